@@ -37,6 +37,11 @@ MOON_DISPATCH_FUSED_DUPS = 0x2  # the default dispatch, named explicitly
 MOON_COMBINE_DUP_PROLOGUE = 0x4
 MOON_DISPATCH_DEDUP_EPILOGUE = 0x8
 
+MOON_DTYPE_F32 = 0
+MOON_DTYPE_BF16 = 1
+MOON_ROUTE_SIGMOID = 0x1
+MOON_ROUTE_RENORM = 0x2
+
 _i32, _u32, _vp = ctypes.c_int32, ctypes.c_uint32, ctypes.c_void_p
 
 
@@ -66,6 +71,15 @@ class moon_grad_tensor(ctypes.Structure):
     _fields_ = [("expert_grads", _vp), ("slot_grads", _vp), ("row_elems", ctypes.c_int64)]
 
 
+class moon_route_config(ctypes.Structure):
+    _fields_ = [(n, _i32) for n in ("R", "S", "E", "K", "dtype")] + \
+               [("flags", _u32), ("scale", ctypes.c_float), ("loss_coef", ctypes.c_float)]
+
+
+class moon_mx4_weight(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("expert_q", "expert_scales", "slot_q", "slot_scales")]
+
+
 _P = ctypes.POINTER
 _lib.moon_ctx_create.argtypes = [_P(moon_config), _P(_vp)]
 _lib.moon_ctx_layout.argtypes = [_vp, _P(moon_layout)]
@@ -87,10 +101,25 @@ _lib.moon_status_str.argtypes = [_i32]
 _lib.moon_status_str.restype = ctypes.c_char_p
 _lib.moon_debug_tile_counts.argtypes = [_vp, _vp, _P(_i32), _P(_i32), _vp]
 _lib.moon_plan_noalloc.argtypes = [_P(moon_config), _vp, _vp, _P(moon_plan_arrays), _vp]
+_i64, _sz = ctypes.c_int64, ctypes.c_size_t
+_lib.moon_route_workspace.argtypes = [_P(moon_route_config), _P(_sz)]
+_lib.moon_route.argtypes = [_P(moon_route_config)] + [_vp] * 10 + [_sz, _vp]
+_lib.moon_route_backward.argtypes = [_P(moon_route_config)] + [_vp] * 9
+_lib.moon_mx4_quantize.argtypes = [_vp, _i32, _i64, _i32, _P(moon_plan_arrays), _vp, _vp, _vp]
+_lib.moon_mx4_dequantize.argtypes = [_vp, _vp, _i64, _i32, _P(moon_plan_arrays), _i32, _vp, _vp]
+_lib.moon_expert_gemm_mx4.argtypes = [_P(moon_plan_arrays), _vp, _vp, _i32, _P(moon_mx4_weight),
+                                      _i32, _vp, _vp]
+_lib.moon_expert_swiglu_mx4.argtypes = [_P(moon_plan_arrays), _vp, _vp, _i32, _P(moon_mx4_weight),
+                                        _P(moon_mx4_weight), _i32, _vp, _vp, _vp]
+_lib.moon_swiglu_save8.argtypes = [_P(moon_plan_arrays), _vp, _vp, _i32, _vp, _vp, _vp, _vp]
+_lib.moon_swiglu_grad8.argtypes = [_P(moon_plan_arrays), _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp]
 for _f in ("moon_ctx_create", "moon_ctx_layout", "moon_plan_create", "moon_plan_clone",
            "moon_plan_view", "moon_plan_status", "moon_plan", "moon_dispatch", "moon_combine",
            "moon_prefetch_index", "moon_prefetch_weight", "moon_reduce_grad",
-           "moon_debug_tile_counts", "moon_plan_noalloc"):
+           "moon_debug_tile_counts", "moon_plan_noalloc", "moon_route_workspace", "moon_route",
+           "moon_route_backward", "moon_mx4_quantize", "moon_mx4_dequantize",
+           "moon_expert_gemm_mx4", "moon_expert_swiglu_mx4", "moon_swiglu_save8",
+           "moon_swiglu_grad8"):
     getattr(_lib, _f).restype = _i32
 
 
@@ -292,6 +321,260 @@ def moon_reduce_grad(ctx, plan, grads, slot_grads, stream=None):
         arr[i] = moon_grad_tensor(pg, ps, n)
     _check(_lib.moon_reduce_grad(ctx.ptr, plan.ptr, arr, len(grads), _stream(stream)),
            "moon_reduce_grad")
+
+
+# ---------------------------------------------------------------------------
+# Routing and expert operators.  `plan` is a Plan, or a dict of the arrays that
+# moon_plan_noalloc filled ("cu_seqlens", "zero_fill_ranges", "experts_to_copy",
+# "status").  All tensors of a call live on one device, which need not be the
+# current one; the stream defaults to that device's current stream.
+_DTYPES = {torch.float32: MOON_DTYPE_F32, torch.bfloat16: MOON_DTYPE_BF16}
+
+
+def _one_device(tensors):
+    """The device index that every given tensor (None skipped) lives on."""
+    dev = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a contiguous CUDA tensor")
+        if dev is None:
+            dev = t.device.index
+        elif t.device.index != dev:
+            raise ValueError(f"{name} is on cuda:{t.device.index}, the call's other tensors on "
+                             f"cuda:{dev}")
+    return dev
+
+
+def _dtype_code(t, name):
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
+    return _DTYPES[t.dtype]
+
+
+def _call(dev, fn, *args, stream=None):
+    """Calls the library with `dev` current (switching to it and back if it is not)."""
+    f = getattr(_lib, fn)
+    if torch.cuda.current_device() == dev:
+        _check(f(*args, _stream(stream)), fn)
+    else:
+        with torch.cuda.device(dev):
+            _check(f(*args, _stream(stream)), fn)
+
+
+def _groups(plan, rows, tensors):
+    """(moon_plan_arrays, device) of a Plan or a dict of plan arrays, for
+    window tensors of `rows` rows."""
+    dev = _one_device(tensors)
+    if isinstance(plan, Plan):
+        pa = moon_plan_view(plan)
+        if plan.ctx.device != dev:
+            raise ValueError(f"the plan is on cuda:{plan.ctx.device}, the tensors on cuda:{dev}")
+    else:
+        cu, etc = plan["cu_seqlens"], plan["experts_to_copy"]
+        if cu.dim() != 2 or etc.dim() != 2 or etc.shape[0] != cu.shape[0] or \
+                cu.shape[1] <= etc.shape[1]:
+            raise ValueError("cu_seqlens must be [R, E+B] and experts_to_copy [R, B]")
+        pa = moon_plan_arrays()
+        pa.R, pa.B = cu.shape[0], etc.shape[1]
+        pa.E = cu.shape[1] - pa.B
+        pa.NvS = rows // pa.R
+        for k, n in (("cu_seqlens", cu.numel()), ("zero_fill_ranges", 2 * cu.numel()),
+                     ("status", 1)):
+            setattr(pa, k, _ptr(plan[k], torch.int32, n, k))
+            if plan[k].device.index != dev:
+                raise ValueError(f"{k} is on {plan[k].device}, the tensors on cuda:{dev}")
+    if rows != pa.R * pa.NvS:
+        raise ValueError(f"window tensors must have R*NvS = {pa.R * pa.NvS} rows, got {rows}")
+    return pa, dev
+
+
+def _route_config(logits, K, flags, scale, loss_coef):
+    if logits.dim() != 3:
+        raise ValueError(f"logits must be [R, S, E], got {tuple(logits.shape)}")
+    R, S, E = logits.shape
+    return moon_route_config(R, S, E, K, _dtype_code(logits, "logits"), flags, scale, loss_coef)
+
+
+def _flags8(valid, n):
+    if valid is None:
+        return None
+    if valid.dtype not in (torch.bool, torch.uint8):
+        raise ValueError(f"valid must be torch.bool or torch.uint8, got {valid.dtype}")
+    return _ptr(valid, valid.dtype, n, "valid")
+
+
+def moon_route(logits, topk, weights, flags=0, scale=1.0, bias=None, valid=None,
+               tokens_per_expert=None, valid_tokens=None, prob_sums=None, loss=None,
+               loss_coef=0.0, workspace=None, stream=None):
+    """Top-k routing of logits [R, S, E] (float32 or bfloat16) into topk
+    [R, S, K] int32 and weights [R, S, K] float32; the optional outputs are
+    described at moon_route in include/moon.h.  workspace: a uint8 tensor of at
+    least moon_route_workspace(...) bytes; allocated for the call when None."""
+    if topk.dim() != 3 or tuple(topk.shape[:2]) != tuple(logits.shape[:2]):
+        raise ValueError(f"topk must be [R, S, K], got {tuple(topk.shape)}")
+    cfg = _route_config(logits, topk.shape[2], flags, scale, loss_coef)
+    R, S, E, K = cfg.R, cfg.S, cfg.E, cfg.K
+    dev = _one_device(dict(logits=logits, topk=topk, weights=weights, bias=bias, valid=valid,
+                           tokens_per_expert=tokens_per_expert, valid_tokens=valid_tokens,
+                           prob_sums=prob_sums, loss=loss, workspace=workspace))
+    if workspace is None and not (tokens_per_expert is None and valid_tokens is None and
+                                  prob_sums is None and loss is None):
+        n = moon_route_workspace(R, S, E, K)
+        if n > 0:
+            workspace = torch.empty(n, dtype=torch.uint8, device=logits.device)
+            if stream is not None:
+                workspace.record_stream(stream)
+    _call(dev, "moon_route", ctypes.byref(cfg), _ptr(logits, logits.dtype, R * S * E, "logits"),
+          _ptr(bias, torch.float32, E, "bias", optional=True), _flags8(valid, R * S),
+          _ptr(topk, torch.int32, R * S * K, "topk"),
+          _ptr(weights, torch.float32, R * S * K, "weights"),
+          _ptr(tokens_per_expert, torch.int32, R * E, "tokens_per_expert", optional=True),
+          _ptr(valid_tokens, torch.int32, R, "valid_tokens", optional=True),
+          _ptr(prob_sums, torch.float32, R * E, "prob_sums", optional=True),
+          _ptr(loss, torch.float32, R, "loss", optional=True),
+          None if workspace is None else _ptr(workspace, torch.uint8, workspace.numel(),
+                                              "workspace"),
+          0 if workspace is None else workspace.numel(), stream=stream)
+
+
+def moon_route_workspace(R, S, E, K):
+    """Bytes of workspace that moon_route needs for these sizes."""
+    cfg = moon_route_config(R, S, E, K, MOON_DTYPE_F32, 0, 1.0, 0.0)
+    n = _sz(0)
+    _check(_lib.moon_route_workspace(ctypes.byref(cfg), ctypes.byref(n)), "moon_route_workspace")
+    return n.value
+
+
+def moon_route_backward(logits, topk, d_logits, flags=0, scale=1.0, valid=None, d_weights=None,
+                        tokens_per_expert=None, valid_tokens=None, d_loss=None, loss_coef=0.0,
+                        stream=None):
+    """Gradient of moon_route to d_logits (the shape and dtype of logits) from
+    d_weights [R, S, K] and d_loss [R], either of which may be None."""
+    if topk.dim() != 3 or tuple(topk.shape[:2]) != tuple(logits.shape[:2]):
+        raise ValueError(f"topk must be [R, S, K], got {tuple(topk.shape)}")
+    cfg = _route_config(logits, topk.shape[2], flags, scale, loss_coef)
+    R, S, E, K = cfg.R, cfg.S, cfg.E, cfg.K
+    dev = _one_device(dict(logits=logits, topk=topk, d_logits=d_logits, valid=valid,
+                           d_weights=d_weights, tokens_per_expert=tokens_per_expert,
+                           valid_tokens=valid_tokens, d_loss=d_loss))
+    _call(dev, "moon_route_backward", ctypes.byref(cfg),
+          _ptr(logits, logits.dtype, R * S * E, "logits"), _flags8(valid, R * S),
+          _ptr(topk, torch.int32, R * S * K, "topk"),
+          _ptr(d_weights, torch.float32, R * S * K, "d_weights", optional=True),
+          _ptr(tokens_per_expert, torch.int32, R * E, "tokens_per_expert", optional=True),
+          _ptr(valid_tokens, torch.int32, R, "valid_tokens", optional=True),
+          _ptr(d_loss, torch.float32, R, "d_loss", optional=True),
+          _ptr(d_logits, logits.dtype, R * S * E, "d_logits"), stream=stream)
+
+
+def _mx4_call(fn, x, q, scales, plan, stream):
+    if x.dim() < 2:
+        raise ValueError("values must be [rows, cols]")
+    cols = x.shape[-1]
+    rows = x.numel() // cols if cols else 0
+    t = dict(values=x, q=q, scales=scales)
+    pa, dev = _groups(plan, rows, t) if plan is not None else (None, _one_device(t))
+    px = _ptr(x, x.dtype, rows * cols, "values")
+    pq = _ptr(q, torch.uint8, rows * (cols // 2), "q")
+    ps = _ptr(scales, torch.uint8, rows * (cols // 32), "scales")
+    code, pp = _dtype_code(x, "values"), None if pa is None else ctypes.byref(pa)
+    if fn == "moon_mx4_quantize":
+        _call(dev, fn, px, code, rows, cols, pp, pq, ps, stream=stream)
+    else:
+        _call(dev, fn, pq, ps, rows, cols, pp, code, px, stream=stream)
+
+
+def moon_mx4_quantize(x, q, scales, plan=None, stream=None):
+    """x [..., cols] (float32 or bfloat16) to MXFP4 codes q [..., cols/2] and
+    scales [..., cols/32] (uint8).  With a plan x is window rows [R*NvS, cols]."""
+    _mx4_call("moon_mx4_quantize", x, q, scales, plan, stream)
+
+
+def moon_mx4_dequantize(q, scales, y, plan=None, stream=None):
+    """The values of MXFP4 codes and scales, to y [..., cols]."""
+    _mx4_call("moon_mx4_dequantize", y, q, scales, plan, stream)
+
+
+def _mx4_weight(pa, w, N, K, name):
+    """moon_mx4_weight of (expert codes, expert scales, slot codes, slot scales)."""
+    eq, es, sq, ss = w
+    E, RB = pa.E, pa.R * pa.B
+    return moon_mx4_weight(_ptr(eq, torch.uint8, E * N * (K // 2), f"{name} expert codes"),
+                           _ptr(es, torch.uint8, E * N * (K // 32), f"{name} expert scales"),
+                           _ptr(sq, torch.uint8, RB * N * (K // 2), f"{name} slot codes"),
+                           _ptr(ss, torch.uint8, RB * N * (K // 32), f"{name} slot scales"))
+
+
+def _rows_of(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [R*NvS, values], got {tuple(t.shape)}")
+    return t.shape
+
+
+def moon_expert_gemm_mx4(plan, xq, xs, weight, y, stream=None):
+    """y [R*NvS, N] bfloat16 = the MXFP4 rows (xq [R*NvS, K/2], xs) times the
+    weights of their groups; weight = (expert_q [E, N, K/2], expert_scales
+    [E, N, K/32], slot_q [R, B, N, K/2], slot_scales [R, B, N, K/32])."""
+    rows, half = _rows_of(xq, "xq")
+    N, K = _rows_of(y, "y")[1], 2 * half
+    pa, dev = _groups(plan, rows, dict(xq=xq, xs=xs, y=y, expert_q=weight[0],
+                                       expert_scales=weight[1], slot_q=weight[2],
+                                       slot_scales=weight[3]))
+    w = _mx4_weight(pa, weight, N, K, "weight")
+    _call(dev, "moon_expert_gemm_mx4", ctypes.byref(pa),
+          _ptr(xq, torch.uint8, rows * half, "xq"), _ptr(xs, torch.uint8, rows * (K // 32), "xs"),
+          K, ctypes.byref(w), N, _ptr(y, torch.bfloat16, rows * N, "y"), stream=stream)
+
+
+def moon_expert_swiglu_mx4(plan, xq, xs, gate, up, h, row_weights=None, stream=None):
+    """h [R*NvS, F] bfloat16: the gated activation of two such products; gate
+    and up as the weight of moon_expert_gemm_mx4, row_weights [R*NvS] float32."""
+    rows, half = _rows_of(xq, "xq")
+    F, K = _rows_of(h, "h")[1], 2 * half
+    t = dict(xq=xq, xs=xs, h=h, row_weights=row_weights)
+    for name, w in (("gate", gate), ("up", up)):
+        t.update({f"{name}[{i}]": x for i, x in enumerate(w)})
+    pa, dev = _groups(plan, rows, t)
+    wg, wu = _mx4_weight(pa, gate, F, K, "gate"), _mx4_weight(pa, up, F, K, "up")
+    _call(dev, "moon_expert_swiglu_mx4", ctypes.byref(pa),
+          _ptr(xq, torch.uint8, rows * half, "xq"), _ptr(xs, torch.uint8, rows * (K // 32), "xs"),
+          K, ctypes.byref(wg), ctypes.byref(wu), F,
+          _ptr(row_weights, torch.float32, rows, "row_weights", optional=True),
+          _ptr(h, torch.bfloat16, rows * F, "h"), stream=stream)
+
+
+def moon_swiglu_save8(plan, gate_up, h, saved, saved_scales, row_weights=None, stream=None):
+    """Gated activation of gate_up [R*NvS, 2F] (gate first) to h [R*NvS, F],
+    both bfloat16, keeping gate_up in 8 bits: saved [R*NvS, 2F] and
+    saved_scales [R*NvS, 2F/32], uint8."""
+    rows, F = _rows_of(h, "h")
+    pa, dev = _groups(plan, rows, dict(gate_up=gate_up, h=h, saved=saved,
+                                       saved_scales=saved_scales, row_weights=row_weights))
+    _call(dev, "moon_swiglu_save8", ctypes.byref(pa),
+          _ptr(gate_up, torch.bfloat16, rows * 2 * F, "gate_up"),
+          _ptr(row_weights, torch.float32, rows, "row_weights", optional=True), F,
+          _ptr(h, torch.bfloat16, rows * F, "h"),
+          _ptr(saved, torch.uint8, rows * 2 * F, "saved"),
+          _ptr(saved_scales, torch.uint8, rows * (2 * F // 32), "saved_scales"), stream=stream)
+
+
+def moon_swiglu_grad8(plan, dh, saved, saved_scales, d_gate_up, row_weights=None,
+                      d_row_weights=None, stream=None):
+    """d_gate_up [R*NvS, 2F] bfloat16 and d_row_weights [R*NvS] float32
+    (optional) from dh [R*NvS, F] and what moon_swiglu_save8 kept."""
+    rows, F = _rows_of(dh, "dh")
+    pa, dev = _groups(plan, rows, dict(dh=dh, saved=saved, saved_scales=saved_scales,
+                                       d_gate_up=d_gate_up, row_weights=row_weights,
+                                       d_row_weights=d_row_weights))
+    _call(dev, "moon_swiglu_grad8", ctypes.byref(pa),
+          _ptr(dh, torch.bfloat16, rows * F, "dh"),
+          _ptr(saved, torch.uint8, rows * 2 * F, "saved"),
+          _ptr(saved_scales, torch.uint8, rows * (2 * F // 32), "saved_scales"),
+          _ptr(row_weights, torch.float32, rows, "row_weights", optional=True), F,
+          _ptr(d_gate_up, torch.bfloat16, rows * 2 * F, "d_gate_up"),
+          _ptr(d_row_weights, torch.float32, rows, "d_row_weights", optional=True), stream=stream)
 
 
 # ---------------------------------------------------------------------------

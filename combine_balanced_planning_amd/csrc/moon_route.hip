@@ -1,0 +1,606 @@
+// moon_route.hip — top-k routing with per-expert counts and a balance loss,
+// and its gradient.
+//
+// For a token with logits x over E experts: scores s = softmax(x) or
+// 1/(1+e^-x), selection key = x (or s + bias with a selection bias), the K
+// largest keys in descending order, the lowest id among equal keys, weights
+// w_k = scale * s[id_k] (/ sum over k).  With p = s / sum(s), P[e] = sum over a
+// rank's valid tokens of p[e], C[e] = their routes to e and n their number,
+//   loss = coef * E / (K n^2) * sum_e C[e] P[e]
+// (C is a count and carries no gradient).  The gradient with G = dL/ds is
+//   softmax: dx = s (G + b - sum_j s_j (G_j + b_j)),
+//   sigmoid: dx = s (1 - s) (G + (b - sum_j p_j b_j) / sum(s)),
+// b[e] = dloss * coef * E / (K n^2) * C[e], G[id_k] = scale * dw_k, or with
+// renormalised weights scale / N * (dw_k - sum_j dw_j s_j / N), N = sum_k s.
+//
+// One wave per token, lane l holds experts l, l + 64, ...: the logits are
+// read once, coalesced, and everything else stays in registers.  Sums over
+// tokens are kept per wave in registers, then per workgroup in LDS, then per
+// workgroup in the workspace, and added in a fixed order at each step, so
+// results repeat bit for bit.
+#include <algorithm>
+
+#include "moon_rows.h"
+
+namespace moon {
+namespace {
+
+constexpr int kMaxWaves = 16;
+constexpr int kMaxExperts = 512;
+constexpr int kMaxTopk = 64;
+
+struct RouteArgs {
+  const void* logits;
+  const float* bias;
+  const uint8_t* valid;
+  int32_t* topk;
+  float* weights;
+  int32_t *counts, *tokens;
+  float *psum, *loss;
+  float* part_p;    // [R][nblk][E]
+  int32_t* part_c;  // [R][nblk][E]
+  int32_t* part_n;  // [R][nblk]
+  int32_t R, S, E, K, nblk;
+  int32_t sigmoid, renorm, stats;
+  float scale, coef;
+};
+
+struct RouteGradArgs {
+  const void* logits;
+  const uint8_t* valid;
+  const int32_t* topk;
+  const float* d_weights;
+  const int32_t *counts, *tokens;
+  const float* d_loss;
+  void* d_logits;
+  int32_t R, S, E, K;
+  int32_t sigmoid, renorm;
+  float scale, coef;
+};
+
+// A float's bits as an unsigned key of the same order: -0 equal to +0, NaN
+// below every number, 0 left over for "no candidate".
+__device__ __forceinline__ uint32_t order_key(float x) {
+  const uint32_t b = __float_as_uint(x + 0.0f);
+  const uint32_t k = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  return x != x ? 1u : k;
+}
+
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+}
+
+template <bool BF16>
+__device__ __forceinline__ float load_logit(const void* base, int64_t i) {
+  if (BF16) return __uint_as_float((uint32_t) static_cast<const uint16_t*>(base)[i] << 16);
+  return static_cast<const float*>(base)[i];
+}
+
+// Takes the largest key (two words when Wide) out of the wave; returns its
+// expert, or -1 when no candidate is left.  Among equal keys the lowest id
+// wins: word j holds ids j*64 .. j*64 + 63 by lane.
+template <int J, bool Wide>
+__device__ __forceinline__ int take_largest(uint32_t (&hi)[J], const uint32_t (&lo)[J], int lane,
+                                            uint32_t* key_out) {
+  uint32_t m = hi[0];
+#pragma unroll
+  for (int j = 1; j < J; ++j) m = max(m, hi[j]);
+  const uint32_t top = wave_max_u32(m);
+  *key_out = top;
+  if (top == 0) return -1;
+  uint32_t low = 0;
+  if (Wide) {
+    uint32_t l = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j) l = max(l, hi[j] == top ? lo[j] : 0u);
+    low = wave_max_u32(l);
+  }
+  int id = -1;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    if (id < 0) {
+      const uint64_t b = __ballot(hi[j] == top && (!Wide || lo[j] == low));
+      if (b != 0) {
+        const int win = __builtin_ctzll(b);
+        id = j * kLanes + win;
+        if (lane == win) hi[j] = 0;
+      }
+    }
+  }
+  return id;
+}
+
+// Selection by score + bias in 64 bits; lane k returns the k-th id.
+template <int J, bool BF16>
+__device__ __attribute__((noinline)) int select_wide(const void* logits, int64_t at,
+                                                     const float* bias, int E, int K, int lane) {
+  uint32_t hi[J], lo[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int e = j * kLanes + lane;
+    hi[j] = lo[j] = 0;
+    if (e < E) {
+      const float x = load_logit<BF16>(logits, at + e);
+      double v = 1.0 / (1.0 + exp(-(double)x)) + (double)bias[e] + 0.0;
+      if (x == -INFINITY) v = -INFINITY;
+      const uint64_t b = (uint64_t)__double_as_longlong(v);
+      const uint64_t k = (b >> 63) != 0 ? ~b : (b | (1ull << 63));
+      hi[j] = v != v ? 1u : (uint32_t)(k >> 32);
+      lo[j] = v != v ? 0u : (uint32_t)k;
+    }
+  }
+  int mine = 0;
+  for (int k = 0; k < K; ++k) {
+    uint32_t top;
+    const int id = take_largest<J, true>(hi, lo, lane, &top);
+    if (lane == k) mine = id;
+  }
+  return mine;
+}
+
+__device__ __forceinline__ float reciprocal_or_zero(float v) {
+  return v > 0.0f ? 1.0f / v : (v == 0.0f ? 0.0f : v);  // NaN stays
+}
+
+// Writes a rank's counts, probability sums, valid tokens and loss.  Called by
+// a whole workgroup; per(e, &p, &c) gives expert e's sums.
+template <class Per>
+__device__ __forceinline__ void finish_rank(const RouteArgs& a, int r, int n, float* red,
+                                            const Per& per) {
+  float part = 0.0f;
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+    float p;
+    int32_t c;
+    per(e, &p, &c);
+    part += p * (float)c;
+    if (a.psum != nullptr) a.psum[r * a.E + e] = p;
+    // tokens outside the batch count as K routes to expert 0, as their ids say
+    if (a.counts != nullptr) a.counts[r * a.E + e] = c + (e == 0 ? a.K * (a.S - n) : 0);
+  }
+  if (a.tokens != nullptr && threadIdx.x == 0) a.tokens[r] = n;
+  if (a.loss != nullptr) {
+    const float ws = wave_sum(part);
+    __syncthreads();
+    if ((threadIdx.x & (kLanes - 1)) == 0) red[threadIdx.x / kLanes] = ws;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      float sum = 0.0f;
+      for (int i = 0; i < (int)blockDim.x / kLanes; ++i) sum += red[i];
+      a.loss[r] = n > 0 ? a.coef * (float)a.E / ((float)a.K * (float)n) * (sum / (float)n) : 0.0f;
+    }
+  }
+}
+
+template <int J, bool BF16>
+__global__ void __launch_bounds__(kMaxWaves* kLanes) k_route(RouteArgs a) {
+  extern __shared__ float lds[];  // with stats: [waves][E] sums, [E] counts, [waves] tokens, [waves]
+  const int lane = threadIdx.x & (kLanes - 1), w = threadIdx.x / kLanes;
+  const int waves = blockDim.x / kLanes;
+  const int r = blockIdx.y, blk = blockIdx.x;
+  float* const red_p = lds;
+  int32_t* const red_c = reinterpret_cast<int32_t*>(lds + waves * a.E);
+  int32_t* const red_n = red_c + a.E;
+  float* const red_l = reinterpret_cast<float*>(red_n + waves);
+  if (a.stats) {
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) red_c[e] = 0;
+    __syncthreads();
+  }
+  const bool biased = a.bias != nullptr;
+  float acc[J], bias[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int e = j * kLanes + lane;
+    acc[j] = 0.0f;
+    bias[j] = biased && e < a.E ? a.bias[e] : 0.0f;
+  }
+  int32_t n_valid = 0;
+  for (int t = blk * waves + w; t < a.S; t += a.nblk * waves) {
+    const int64_t tok = (int64_t)r * a.S + t;
+    const int64_t at = tok * a.E;
+    if (a.valid != nullptr && a.valid[tok] == 0) {  // one token, so the whole wave agrees
+      if (lane < a.K) {
+        a.topk[tok * a.K + lane] = 0;
+        a.weights[tok * a.K + lane] = 0.0f;
+      }
+      continue;
+    }
+    ++n_valid;
+    float s[J];
+    uint32_t key[J];
+    float shift = 0.0f;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int e = j * kLanes + lane;
+      s[j] = e < a.E ? load_logit<BF16>(a.logits, at + e) : 0.0f;
+      key[j] = e < a.E ? order_key(s[j]) : 0u;
+    }
+    if (a.sigmoid) {
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const float x = s[j];
+        s[j] = sigmoid_f32(x);
+        if (biased && key[j] != 0u && x != -INFINITY) key[j] = order_key(s[j] + bias[j]);
+      }
+    } else {
+      uint32_t m = key[0];
+#pragma unroll
+      for (int j = 1; j < J; ++j) m = max(m, key[j]);
+      m = wave_max_u32(m);
+      // Nothing but masked experts or NaN: scores 0 (NaN) with no shift.
+      const float top = key_value(m);
+      shift = m == 1u || top == -INFINITY ? 0.0f : top;
+#pragma unroll
+      for (int j = 0; j < J; ++j) s[j] = exp_f32(s[j] - shift);
+    }
+    float total = 0.0f;
+    if (a.stats || !a.renorm) {
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        if (j * kLanes + lane >= a.E) s[j] = 0.0f;
+        total += s[j];
+      }
+      total = wave_sum(total);
+    }
+    int mine = 0;
+    uint32_t my_key = 0;
+    float prev = 0.0f;
+    bool close = false;
+    for (int k = 0; k < a.K; ++k) {
+      uint32_t top;
+      const int id = take_largest<J, false>(key, key, lane, &top);
+      if (lane == k) {
+        mine = id;
+        my_key = top;
+      }
+      const float v = key_value(top);
+      close = close || (k > 0 && prev - v <= 1e-6f * fmaxf(1.0f, fabsf(v)));
+      prev = v;
+    }
+    float sel;
+    if (biased) {
+      uint32_t next = key[0];
+#pragma unroll
+      for (int j = 1; j < J; ++j) next = max(next, key[j]);
+      const float v = key_value(wave_max_u32(next));
+      close = close || prev - v <= 1e-6f * fmaxf(1.0f, fabsf(v));
+      // A score in 32 bits plus its bias is off by a few units in the last
+      // place, below 5e-7 * max(1, |sum|): neighbours nearer than twice that
+      // are told apart in 64 bits.
+      if (close) mine = select_wide<J, BF16>(a.logits, at, a.bias, a.E, a.K, lane);
+      sel = lane < a.K ? sigmoid_f32(load_logit<BF16>(a.logits, at + mine)) : 0.0f;
+    } else {
+      const float x = my_key == 1u ? NAN : key_value(my_key);
+      sel = lane < a.K ? (a.sigmoid ? sigmoid_f32(x) : exp_f32(x - shift)) : 0.0f;
+    }
+    float out;
+    if (a.renorm)
+      out = a.scale * (sel * reciprocal_or_zero(wave_sum(sel)));
+    else
+      out = a.scale * (a.sigmoid ? sel : sel * reciprocal_or_zero(total));
+    if (lane < a.K) {
+      a.topk[tok * a.K + lane] = mine;
+      a.weights[tok * a.K + lane] = out;
+    }
+    if (a.stats) {
+      const float inv = reciprocal_or_zero(total);
+#pragma unroll
+      for (int j = 0; j < J; ++j) acc[j] += s[j] * inv;
+      if (lane < a.K) atomicAdd(&red_c[mine], 1);  // whole numbers: any order
+    }
+  }
+  if (!a.stats) return;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int e = j * kLanes + lane;
+    if (e < a.E) red_p[w * a.E + e] = acc[j];
+  }
+  if (lane == 0) red_n[w] = n_valid;
+  __syncthreads();
+  int32_t n = 0;
+  for (int i = 0; i < waves; ++i) n += red_n[i];
+  const auto per = [&](int e, float* p, int32_t* c) {
+    float sum = 0.0f;
+    for (int i = 0; i < waves; ++i) sum += red_p[i * a.E + e];
+    *p = sum;
+    *c = red_c[e];
+  };
+  if (a.nblk == 1) {
+    finish_rank(a, r, n, red_l, per);
+    return;
+  }
+  const int64_t row = (int64_t)r * a.nblk + blk;
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x)
+    per(e, &a.part_p[row * a.E + e], &a.part_c[row * a.E + e]);
+  if (threadIdx.x == 0) a.part_n[row] = n;
+}
+
+__global__ void __launch_bounds__(kMaxExperts) k_route_finish(RouteArgs a) {
+  __shared__ float red[kMaxExperts / kLanes];
+  const int r = blockIdx.x;
+  const int64_t row = (int64_t)r * a.nblk;
+  int32_t n = 0;
+  for (int i = 0; i < a.nblk; ++i) n += a.part_n[row + i];
+  finish_rank(a, r, n, red, [&](int e, float* p, int32_t* c) {
+    float sum = 0.0f;
+    int32_t cnt = 0;
+#pragma unroll 8
+    for (int i = 0; i < a.nblk; ++i) {
+      sum += a.part_p[(row + i) * a.E + e];
+      cnt += a.part_c[(row + i) * a.E + e];
+    }
+    *p = sum;
+    *c = cnt;
+  });
+}
+
+template <int J, bool BF16>
+__global__ void __launch_bounds__(256) k_route_grad(RouteGradArgs a, int nblk) {
+  __shared__ float lds[4][J * kLanes];
+  const int lane = threadIdx.x & (kLanes - 1), w = threadIdx.x / kLanes;
+  const int r = blockIdx.y;
+  float b[J];
+  {
+    float base = 0.0f;
+    if (a.d_loss != nullptr) {
+      const float n = (float)a.tokens[r];
+      if (n > 0.0f) base = a.d_loss[r] * (a.coef * (float)a.E / ((float)a.K * n) / n);
+    }
+    const int32_t pads = a.d_loss != nullptr ? a.K * (a.S - a.tokens[r]) : 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int e = j * kLanes + lane;
+      b[j] = a.d_loss != nullptr && e < a.E
+                 ? base * (float)(a.counts[r * a.E + e] - (e == 0 ? pads : 0)) : 0.0f;
+    }
+  }
+  for (int t = blockIdx.x * 4 + w; t < a.S; t += nblk * 4) {
+    const int64_t tok = (int64_t)r * a.S + t;
+    const int64_t at = tok * a.E;
+    float d[J];
+    if (a.valid != nullptr && a.valid[tok] == 0) {
+#pragma unroll
+      for (int j = 0; j < J; ++j) d[j] = 0.0f;
+    } else {
+      float s[J], x[J];
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int e = j * kLanes + lane;
+        x[j] = e < a.E ? load_logit<BF16>(a.logits, at + e) : -INFINITY;
+        lds[w][e] = 0.0f;
+        if (e < a.E) m = max(m, order_key(x[j]));
+      }
+      float shift = 0.0f;
+      if (!a.sigmoid) {
+        m = wave_max_u32(m);
+        const float top = key_value(m);
+        shift = m == 1u || top == -INFINITY ? 0.0f : top;
+      }
+      float total = 0.0f;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        s[j] = a.sigmoid ? sigmoid_f32(x[j]) : exp_f32(x[j] - shift);
+        total += s[j];
+      }
+      total = wave_sum(total);
+      const float inv = reciprocal_or_zero(total);
+      if (a.d_weights != nullptr) {
+        const int id = lane < a.K ? a.topk[tok * a.K + lane] : -1;
+        const bool ok = id >= 0 && id < a.E;
+        const float dw = ok ? a.d_weights[tok * a.K + lane] : 0.0f;
+        float sel = 0.0f;
+        if (ok) {
+          const float v = load_logit<BF16>(a.logits, at + id);
+          sel = a.sigmoid ? sigmoid_f32(v) : exp_f32(v - shift);
+        }
+        float g;
+        if (a.renorm) {
+          const float rn = reciprocal_or_zero(wave_sum(sel));
+          const float mean = wave_sum(dw * (sel * rn));
+          g = a.scale * rn * (dw - mean);
+        } else {
+          g = a.scale * dw;
+        }
+        // softmax scores are total times the ones above: dL/ds of those
+        if (!a.sigmoid && !a.renorm) g *= inv;
+        wave_lds_sync();
+        if (ok) atomicAdd(&lds[w][id], g);
+      }
+      wave_lds_sync();
+      // s, total and G now go by unnormalised scores; p = s * inv
+      float dot = 0.0f;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const float g = lds[w][j * kLanes + lane];
+        d[j] = g;
+        dot += a.sigmoid ? s[j] * inv * b[j] : s[j] * g + s[j] * inv * b[j];
+      }
+      dot = wave_sum(dot);
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        if (a.sigmoid)
+          d[j] = s[j] * sigmoid_f32(-x[j]) * (d[j] + (b[j] - dot) * inv);
+        else
+          d[j] = s[j] * (d[j] + (b[j] - dot) * inv);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int e = j * kLanes + lane;
+      if (e < a.E) {
+        if (BF16)
+          static_cast<uint16_t*>(a.d_logits)[at + e] = (uint16_t)pack_bf16(d[j], 0.0f);
+        else
+          static_cast<float*>(a.d_logits)[at + e] = d[j];
+      }
+    }
+  }
+}
+
+// How a call is cut: waves per workgroup and workgroups per rank.  Up to 256
+// tokens a rank one workgroup of 16 waves does it all in one launch; beyond
+// that workgroups of four waves, enough to fill the GPU (2048 in all), and a
+// second launch adds their partial sums.  Without counts, sums or loss there
+// is nothing to add and every four tokens get a workgroup.
+void route_cut(int R, int S, bool stats, int* waves, int* nblk) {
+  if (stats && S <= 256) {
+    *waves = std::min(kMaxWaves, S);
+    *nblk = 1;
+    return;
+  }
+  *waves = 4;
+  const int want = (S + 3) / 4;
+  *nblk = stats ? std::max(1, std::min(want, 2048 / R)) : std::min(want, 65536);
+}
+
+size_t route_workspace(int R, int S, int E, bool stats) {
+  int waves, nblk;
+  route_cut(R, S, stats, &waves, &nblk);
+  return nblk == 1 || !stats ? 0 : (size_t)R * nblk * (2 * (size_t)E + 1) * 4;
+}
+
+template <int J, bool BF16>
+hipError_t run_route(const RouteArgs& a, int waves, hipStream_t s) {
+  const size_t lds = a.stats ? ((size_t)waves * a.E + a.E + 2 * waves) * 4 : 0;
+  hipLaunchKernelGGL((k_route<J, BF16>), dim3(a.nblk, a.R), dim3(waves * kLanes), lds, s, a);
+  if (a.stats && a.nblk > 1)
+    hipLaunchKernelGGL(k_route_finish, dim3(a.R), dim3((a.E + kLanes - 1) / kLanes * kLanes), 0, s,
+                       a);
+  return hipGetLastError();
+}
+
+template <int J, bool BF16>
+hipError_t run_route_grad(const RouteGradArgs& a, hipStream_t s) {
+  const int nblk = std::max(1, std::min((a.S + 3) / 4, 4096 / a.R));
+  hipLaunchKernelGGL((k_route_grad<J, BF16>), dim3(nblk, a.R), dim3(256), 0, s, a, nblk);
+  return hipGetLastError();
+}
+
+// Words of 64 experts per token, rounded to the instantiated counts.
+#define MOON_BY_WORDS(J_, FN, BF, ...)                         \
+  (J_ <= 1 ? FN<1, BF>(__VA_ARGS__) : J_ <= 2 ? FN<2, BF>(__VA_ARGS__) \
+   : J_ <= 3 ? FN<3, BF>(__VA_ARGS__) : J_ <= 4 ? FN<4, BF>(__VA_ARGS__) \
+   : J_ <= 6 ? FN<6, BF>(__VA_ARGS__) : FN<8, BF>(__VA_ARGS__))
+
+moon_status check_config(const moon_route_config* c) {
+  if (c == nullptr || (c->flags & ~(MOON_ROUTE_SIGMOID | MOON_ROUTE_RENORM)) != 0)
+    return MOON_ERR_INVALID_ARG;
+  if (c->dtype != MOON_DTYPE_F32 && c->dtype != MOON_DTYPE_BF16) return MOON_ERR_INVALID_ARG;
+  if (c->R < 1 || c->S < 1 || c->E < 1 || c->K < 1 || c->K > c->E) return MOON_ERR_INVALID_ARG;
+  if (c->R > 32 || c->E > kMaxExperts || c->K > kMaxTopk ||
+      (int64_t)c->R * c->S * c->K >= (int64_t)1 << 31)
+    return MOON_ERR_UNSUPPORTED;
+  return MOON_OK;
+}
+
+}  // namespace
+}  // namespace moon
+
+extern "C" {
+
+moon_status moon_route_workspace(const moon_route_config* cfg, size_t* bytes) {
+  if (bytes == nullptr) return MOON_ERR_INVALID_ARG;
+  *bytes = 0;
+  const moon_status st = moon::check_config(cfg);
+  if (st != MOON_OK) return st;
+  *bytes = moon::route_workspace(cfg->R, cfg->S, cfg->E, true);
+  return MOON_OK;
+}
+
+moon_status moon_route(const moon_route_config* cfg, const void* logits_rse, const float* bias_e,
+                       const uint8_t* valid_rs, int32_t* topk_rsk, float* weights_rsk,
+                       int32_t* tokens_per_expert_re, int32_t* valid_tokens_r,
+                       float* prob_sums_re, float* loss_r, void* workspace,
+                       size_t workspace_bytes, hipStream_t stream) {
+  using moon::is_aligned;
+  const moon_status st = moon::check_config(cfg);
+  if (st != MOON_OK) return st;
+  if (logits_rse == nullptr || topk_rsk == nullptr || weights_rsk == nullptr)
+    return MOON_ERR_INVALID_ARG;
+  if (bias_e != nullptr && (cfg->flags & MOON_ROUTE_SIGMOID) == 0) return MOON_ERR_INVALID_ARG;
+  if (!is_aligned(logits_rse, cfg->dtype == MOON_DTYPE_F32 ? 4 : 2) || !is_aligned(bias_e, 4) ||
+      !is_aligned(topk_rsk, 4) || !is_aligned(weights_rsk, 4) ||
+      !is_aligned(tokens_per_expert_re, 4) || !is_aligned(valid_tokens_r, 4) ||
+      !is_aligned(prob_sums_re, 4) || !is_aligned(loss_r, 4) || !is_aligned(workspace, 4))
+    return MOON_ERR_INVALID_ARG;
+  moon::RouteArgs a = {};
+  a.logits = logits_rse;
+  a.bias = bias_e;
+  a.valid = valid_rs;
+  a.topk = topk_rsk;
+  a.weights = weights_rsk;
+  a.counts = tokens_per_expert_re;
+  a.tokens = valid_tokens_r;
+  a.psum = prob_sums_re;
+  a.loss = loss_r;
+  a.R = cfg->R;
+  a.S = cfg->S;
+  a.E = cfg->E;
+  a.K = cfg->K;
+  a.sigmoid = (cfg->flags & MOON_ROUTE_SIGMOID) != 0;
+  a.renorm = (cfg->flags & MOON_ROUTE_RENORM) != 0;
+  a.scale = cfg->scale;
+  a.coef = cfg->loss_coef;
+  a.stats = tokens_per_expert_re != nullptr || valid_tokens_r != nullptr ||
+            prob_sums_re != nullptr || loss_r != nullptr;
+  int waves;
+  moon::route_cut(a.R, a.S, a.stats != 0, &waves, &a.nblk);
+  const size_t need = moon::route_workspace(a.R, a.S, a.E, a.stats != 0);
+  if (need > 0) {
+    if (workspace == nullptr || workspace_bytes < need) return MOON_ERR_INVALID_ARG;
+    const size_t n = (size_t)a.R * a.nblk * a.E;
+    a.part_p = static_cast<float*>(workspace);
+    a.part_c = reinterpret_cast<int32_t*>(a.part_p + n);
+    a.part_n = a.part_c + n;
+  }
+  const int J = (a.E + moon::kLanes - 1) / moon::kLanes;
+  using namespace moon;
+  const hipError_t e = cfg->dtype == MOON_DTYPE_BF16
+                           ? MOON_BY_WORDS(J, run_route, true, a, waves, stream)
+                           : MOON_BY_WORDS(J, run_route, false, a, waves, stream);
+  return e == hipSuccess ? MOON_OK : MOON_ERR_HIP;
+}
+
+moon_status moon_route_backward(const moon_route_config* cfg, const void* logits_rse,
+                                const uint8_t* valid_rs, const int32_t* topk_rsk,
+                                const float* d_weights_rsk, const int32_t* tokens_per_expert_re,
+                                const int32_t* valid_tokens_r, const float* d_loss_r,
+                                void* d_logits_rse, hipStream_t stream) {
+  using moon::is_aligned;
+  const moon_status st = moon::check_config(cfg);
+  if (st != MOON_OK) return st;
+  if (logits_rse == nullptr || d_logits_rse == nullptr) return MOON_ERR_INVALID_ARG;
+  if (d_weights_rsk != nullptr && topk_rsk == nullptr) return MOON_ERR_INVALID_ARG;
+  if (d_loss_r != nullptr && (tokens_per_expert_re == nullptr || valid_tokens_r == nullptr))
+    return MOON_ERR_INVALID_ARG;
+  const uintptr_t el = cfg->dtype == MOON_DTYPE_F32 ? 4 : 2;
+  if (!is_aligned(logits_rse, el) || !is_aligned(d_logits_rse, el) || !is_aligned(topk_rsk, 4) ||
+      !is_aligned(d_weights_rsk, 4) || !is_aligned(tokens_per_expert_re, 4) ||
+      !is_aligned(valid_tokens_r, 4) || !is_aligned(d_loss_r, 4))
+    return MOON_ERR_INVALID_ARG;
+  moon::RouteGradArgs a = {};
+  a.logits = logits_rse;
+  a.valid = valid_rs;
+  a.topk = topk_rsk;
+  a.d_weights = d_weights_rsk;
+  a.counts = tokens_per_expert_re;
+  a.tokens = valid_tokens_r;
+  a.d_loss = d_loss_r;
+  a.d_logits = d_logits_rse;
+  a.R = cfg->R;
+  a.S = cfg->S;
+  a.E = cfg->E;
+  a.K = cfg->K;
+  a.sigmoid = (cfg->flags & MOON_ROUTE_SIGMOID) != 0;
+  a.renorm = (cfg->flags & MOON_ROUTE_RENORM) != 0;
+  a.scale = cfg->scale;
+  a.coef = cfg->loss_coef;
+  const int J = (a.E + moon::kLanes - 1) / moon::kLanes;
+  using namespace moon;
+  const hipError_t e = cfg->dtype == MOON_DTYPE_BF16
+                           ? MOON_BY_WORDS(J, run_route_grad, true, a, stream)
+                           : MOON_BY_WORDS(J, run_route_grad, false, a, stream);
+  return e == hipSuccess ? MOON_OK : MOON_ERR_HIP;
+}
+
+}  // extern "C"

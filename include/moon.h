@@ -41,6 +41,7 @@
 #ifndef MOON_H
 #define MOON_H
 
+#include <stddef.h>
 #include <stdint.h>
 #include <hip/hip_runtime_api.h>
 
@@ -269,6 +270,145 @@ typedef struct {
 moon_status moon_reduce_grad(moon_ctx* ctx, const moon_comm_plan* plan,
                              const moon_grad_tensor* tensors, int32_t n_tensors,
                              hipStream_t stream);
+
+/* ---- Routing and expert operators ----
+ *
+ * What stands before moon_plan (the router) and between moon_dispatch and
+ * moon_combine (the experts).  They need no context and allocate nothing.
+ * Those that walk the window rows take the plan's arrays (moon_plan_view, or
+ * the caller's own of moon_plan_noalloc) and read cu_seqlens, zero_fill_ranges,
+ * status, R, E, B and NvS of them; the other fields may be null.  The arrays
+ * are laid out as the planner does: rank u's rows belong to its own experts
+ * u*E/R ... and to its slots.  A plan whose device status is not OK
+ * writes nothing.  Rows that hold routes are computed, padding rows of the
+ * result are zeroed without being read, rows behind a rank's last group are
+ * neither read nor written.  Outputs must not overlap inputs.  The caller's
+ * current device is the one that the pointers and the stream belong to.
+ */
+
+typedef enum { MOON_DTYPE_F32 = 0, MOON_DTYPE_BF16 = 1 } moon_dtype;
+
+/* Routing flags.  Scores are softmax(logits), or 1/(1+exp(-logit)) with
+ * MOON_ROUTE_SIGMOID; MOON_ROUTE_RENORM divides a token's K weights by their
+ * sum. */
+#define MOON_ROUTE_SIGMOID 0x1u
+#define MOON_ROUTE_RENORM 0x2u
+
+/* R ranks of S tokens with E logits each, K experts per token; dtype (a
+ * moon_dtype) is that of the logits and their gradient.  Limits: R <= 32,
+ * K <= E <= 512, K <= 64, R*S*K < 2^31. */
+typedef struct {
+  int32_t R, S, E, K, dtype;
+  uint32_t flags;
+  float scale;     /* factor of the weights */
+  float loss_coef; /* factor of the balance loss */
+} moon_route_config;
+
+/* Bytes that moon_route needs as workspace for cfg (0 for a short S); enough
+ * for any set of outputs. */
+moon_status moon_route_workspace(const moon_route_config* cfg, size_t* bytes);
+
+/* Top-k routing.  For every token: topk_rsk [R,S,K] the ids of its K largest
+ * logits, in descending order, the lower id first among equals (with bias_e
+ * [E] fp32, MOON_ROUTE_SIGMOID only: of its K largest score + bias), and
+ * weights_rsk [R,S,K] fp32 = scale * score (divided by their sum with
+ * MOON_ROUTE_RENORM).  Two ids of a token never agree.  A logit of -infinity
+ * masks its expert: score 0, picked only when fewer than K others are left; a
+ * sum of scores that is 0 gives weights 0.  A NaN logit ranks last
+ * and makes NaN what its score enters (weights renormalised over picked
+ * experts only where it is picked).
+ * valid_rs [R,S] (optional): a 0 marks a token outside the batch, whose logits
+ * are not read, whose ids and weights are 0 and which the balance leaves out.
+ * Optional outputs, NULL where not wanted:
+ *   tokens_per_expert_re [R,E]  histogram of the ids written (the marked
+ *                               tokens' zeros included): moon_plan's input
+ *   valid_tokens_r [R]          tokens inside the batch, n
+ *   prob_sums_re [R,E] fp32     P[e] = sum over those of score_e / sum(score)
+ *   loss_r [R] fp32             loss_coef * E / (K n^2) * sum_e C[e] P[e],
+ *                               C[e] = their routes to e; 0 when n = 0
+ * workspace: 4-byte aligned device memory that no overlapping call uses;
+ * needed when one of these is wanted and moon_route_workspace is not 0.
+ * Results repeat bit for bit. */
+moon_status moon_route(const moon_route_config* cfg, const void* logits_rse, const float* bias_e,
+                       const uint8_t* valid_rs, int32_t* topk_rsk, float* weights_rsk,
+                       int32_t* tokens_per_expert_re, int32_t* valid_tokens_r,
+                       float* prob_sums_re, float* loss_r, void* workspace,
+                       size_t workspace_bytes, hipStream_t stream);
+
+/* Gradient of moon_route: d_logits_rse [R,S,E] (written whole) from
+ * d_weights_rsk [R,S,K] fp32 (or NULL) at the ids topk_rsk, and from d_loss_r
+ * [R] fp32 (or NULL) with the counts and valid tokens that moon_route wrote.
+ * The ids and counts carry no gradient; tokens outside the batch get 0. */
+moon_status moon_route_backward(const moon_route_config* cfg, const void* logits_rse,
+                                const uint8_t* valid_rs, const int32_t* topk_rsk,
+                                const float* d_weights_rsk, const int32_t* tokens_per_expert_re,
+                                const int32_t* valid_tokens_r, const float* d_loss_r,
+                                void* d_logits_rse, hipStream_t stream);
+
+/* Rows to microscaled 4-bit floating point (OCP MXFP4): x [rows, cols] of
+ * dtype to q [rows, cols/2] (value 2i in the low half of byte i) and scales
+ * [rows, cols/32].  32 neighbouring values share the scale 2^(byte - 127) with
+ * byte = max(floor(log2(largest magnitude)) - 2, -127) + 127; a value over its
+ * scale is rounded to nearest even e2m1 and saturates at 6.  A block that
+ * holds an infinity or a NaN gets the byte 255.  cols is a multiple of 32, at
+ * most 65536, rows < 2^31; x and q 16-byte aligned.  plan NULL: every row
+ * (weights); else x is the window rows [R*NvS, cols], of which those that hold
+ * routes are converted. */
+moon_status moon_mx4_quantize(const void* x, int32_t dtype, int64_t rows, int32_t cols,
+                              const moon_plan_arrays* plan, uint8_t* q, uint8_t* scales,
+                              hipStream_t stream);
+
+/* The values that q and scales stand for, to y [rows, cols] of dtype (exact;
+ * NaN where the scale byte is 255). */
+moon_status moon_mx4_dequantize(const uint8_t* q, const uint8_t* scales, int64_t rows,
+                                int32_t cols, const moon_plan_arrays* plan, int32_t dtype,
+                                void* y, hipStream_t stream);
+
+/* One MXFP4 expert weight, split like moon_weight_tensor (moon_prefetch_weight
+ * copies codes and scales into the slots as two of its tensors):
+ *   expert_q [E, N, K/2], expert_scales [E, N, K/32]        the experts
+ *   slot_q [R, B, N, K/2], slot_scales [R, B, N, K/32]      the slots
+ * codes 16-byte aligned. */
+typedef struct {
+  const uint8_t *expert_q, *expert_scales, *slot_q, *slot_scales;
+} moon_mx4_weight;
+
+/* Product of every group's rows with its expert's weight: y [R*NvS, N] bf16,
+ * y[row][n] = sum over k of x[row][k] * w[n][k], summed in fp32 and rounded
+ * once; x = (xq, xs) as moon_mx4_quantize writes window rows.  K is a
+ * multiple of 32, N of 8, both at most 65536. */
+moon_status moon_expert_gemm_mx4(const moon_plan_arrays* plan, const uint8_t* xq,
+                                 const uint8_t* xs, int32_t K, const moon_mx4_weight* w, int32_t N,
+                                 void* y, hipStream_t stream);
+
+/* Gate and up products with the gated activation: h [R*NvS, F] bf16,
+ * h[row][f] = c * G / (1 + exp(-G)) * U with the fp32 products G (gate) and U
+ * (up) and c = row_weights[row] ([R*NvS] fp32, e.g. the weight windows), or 1
+ * when NULL.  With the weights applied here the combine is unweighted. */
+moon_status moon_expert_swiglu_mx4(const moon_plan_arrays* plan, const uint8_t* xq,
+                                   const uint8_t* xs, int32_t K, const moon_mx4_weight* gate,
+                                   const moon_mx4_weight* up, int32_t F, const float* row_weights,
+                                   void* h, hipStream_t stream);
+
+/* The gated activation for training, its inputs kept in 8 bits: from gate_up
+ * [R*NvS, 2F] bf16 (gate values first) h [R*NvS, F] bf16 = c * g / (1 +
+ * exp(-g)) * u, c = row_weights[row] or 1, and saved [R*NvS, 2F] with
+ * saved_scales [R*NvS, 2F/32]: e4m3 values, 32 of them under the smallest
+ * scale 2^(byte - 127) that holds the largest (at most 448 of it), rounded to
+ * nearest even; byte 255 marks a block with an infinity or a NaN.  saved is
+ * not written at padding rows.  F is a multiple of 32, at most 65536; gate_up,
+ * h and saved 16-byte aligned. */
+moon_status moon_swiglu_save8(const moon_plan_arrays* plan, const void* gate_up,
+                              const float* row_weights, int32_t F, void* h, uint8_t* saved,
+                              uint8_t* saved_scales, hipStream_t stream);
+
+/* Its gradient with g and u as the saved values: d_gate_up [R*NvS, 2F] bf16
+ * from dh [R*NvS, F] bf16, and d_row_weights [R*NvS] fp32 (or NULL; 0 at
+ * padding rows), the sum over f of dh * g / (1 + exp(-g)) * u.  moon_combine's
+ * weight gather takes d_row_weights back to [R,S,K] for moon_route_backward. */
+moon_status moon_swiglu_grad8(const moon_plan_arrays* plan, const void* dh, const uint8_t* saved,
+                              const uint8_t* saved_scales, const float* row_weights, int32_t F,
+                              void* d_gate_up, float* d_row_weights, hipStream_t stream);
 
 const char* moon_status_str(moon_status s);
 
