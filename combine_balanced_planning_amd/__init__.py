@@ -326,7 +326,7 @@ def moon_reduce_grad(ctx, plan, grads, slot_grads, stream=None):
 # ---------------------------------------------------------------------------
 # Routing and expert operators.  `plan` is a Plan, or a dict of the arrays that
 # moon_plan_noalloc filled ("cu_seqlens", "zero_fill_ranges", "experts_to_copy",
-# "status").  All tensors of a call live on one device, which need not be the
+# "status"; "dst" where at hand, for its size).  All tensors of a call live on one device, which need not be the
 # current one; the stream defaults to that device's current stream.
 _DTYPES = {torch.float32: MOON_DTYPE_F32, torch.bfloat16: MOON_DTYPE_BF16}
 
@@ -380,6 +380,7 @@ def _groups(plan, rows, tensors):
         pa.R, pa.B = cu.shape[0], etc.shape[1]
         pa.E = cu.shape[1] - pa.B
         pa.NvS = rows // pa.R
+        pa.N = plan["dst"].numel() // pa.R if "dst" in plan else 0
         for k, n in (("cu_seqlens", cu.numel()), ("zero_fill_ranges", 2 * cu.numel()),
                      ("status", 1)):
             setattr(pa, k, _ptr(plan[k], torch.int32, n, k))

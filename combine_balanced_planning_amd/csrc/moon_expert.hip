@@ -23,6 +23,7 @@ namespace {
 
 typedef int vec8i __attribute__((ext_vector_type(8)));
 typedef float vec4f __attribute__((ext_vector_type(4)));
+typedef float vec16f __attribute__((ext_vector_type(16)));
 
 struct Weight {
   const uint8_t *eq, *es, *sq, *ss;  // experts' codes and scales, slots' codes and scales
@@ -160,6 +161,370 @@ __global__ void __launch_bounds__(256) k_expert_stream(ExpertArgs a, Groups g) {
   }
 }
 
+// ---- many rows per group: tiles of 256 weight rows by 256 window rows ----
+
+constexpr int kTileThreads = 256;
+constexpr int kTile = 256;
+constexpr int kMaxEntries = 2048;  // of the tile table
+
+// 16 bytes per lane from global memory straight into LDS, lane l at dst + 16 l.
+__device__ __forceinline__ void load_lds16(const uint8_t* src, vec4u* dst) {
+  __builtin_amdgcn_global_load_lds(
+      (const __attribute__((address_space(1))) void*)src,
+      (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+}
+
+// Waits until at most n vector memory operations of this wave are in flight.
+template <int n>
+__device__ __forceinline__ void wait_vm() {
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (n & 15) | ((n >> 4) << 14));
+}
+__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(0xC07F); }
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// One tile of results; every field is the same in all lanes.
+struct Tile {
+  int u, j;          // rank and entry
+  int row0, n0;      // first window row (local) and first output
+  int rows;          // rows from row0 to the group's last route
+  int pad;           // padding rows to clear behind them, 0 but for the last row tile
+};
+
+// Scale bytes of 512 values (16 blocks) as the matrix cores take them: word kb
+// holds the blocks kb, 4 + kb, 8 + kb, 12 + kb, the lane group's block in each
+// of four steps.
+__device__ __forceinline__ vec4u transpose_scales(vec4u d) {
+  const uint32_t a0 = __builtin_amdgcn_perm(d.y, d.x, 0x05010400u);  // x0 y0 x1 y1
+  const uint32_t a1 = __builtin_amdgcn_perm(d.y, d.x, 0x07030602u);  // x2 y2 x3 y3
+  const uint32_t b0 = __builtin_amdgcn_perm(d.w, d.z, 0x05010400u);
+  const uint32_t b1 = __builtin_amdgcn_perm(d.w, d.z, 0x07030602u);
+  const vec4u o = {__builtin_amdgcn_perm(b0, a0, 0x05040100u),
+                   __builtin_amdgcn_perm(b0, a0, 0x07060302u),
+                   __builtin_amdgcn_perm(b1, a1, 0x05040100u),
+                   __builtin_amdgcn_perm(b1, a1, 0x07060302u)};
+  return o;
+}
+
+template <int Step>
+__device__ __forceinline__ vec16f mfma32(vec4u a, vec4u b, vec16f c, uint32_t sa, uint32_t sb) {
+  const vec8i av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+  const vec8i bv = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, Step, (int)sa, Step,
+                                                         (int)sb);
+}
+
+// Half a step of a wave (64 values): 16 products of its four weight and four
+// row fragments f, while the fragments n of the next half come from LDS.  The
+// schedule puts two reads before each of the first four pairs of products, so
+// they have arrived when the half ends.
+template <int Step>
+__device__ __forceinline__ void half_step(const vec4u* wsrc, const vec4u* xsrc, const vec4u (&f)[8],
+                                          vec4u (&n)[8], const uint32_t (&s)[8],
+                                          vec16f (&acc)[4][4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) n[i] = wsrc[i * 2 * kLanes];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) n[4 + i] = xsrc[i * 2 * kLanes];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      acc[i][k] = mfma32<Step>(f[i], f[4 + k], acc[i][k], s[i], s[4 + k]);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    if (k < 4) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+  }
+}
+
+// A workgroup of four waves (one per SIMD) walks tiles of 256 weight rows by
+// 256 window rows; each wave owns 128 by 128 of them (256 accumulators a lane,
+// v_mfma_scale_f32_32x32x64).  K advances by 128 values a step, four steps to a
+// turn of 512.  LDS holds four steps of both operands: global_load_lds writes
+// 16 rows by four scale blocks in lane order, ds_read_b128 takes them out
+// without bank conflicts.  Each step refills the buffer it has just emptied
+// with the same step of the next turn, which may belong to the next tile: the
+// loads run three steps ahead without a pause at tile borders.  The weight rows
+// of a fragment are dealt so that a lane ends up with 64 neighbouring outputs
+// (32 with a gate) of four window rows.
+template <bool Swiglu, bool Whole>
+__global__ void __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
+    k_expert_tiles(ExpertArgs a, Groups g) {
+  constexpr int kOut = Swiglu ? kTile / 2 : kTile;  // outputs per tile
+  __shared__ vec4u st0[32 * kLanes], st1[32 * kLanes], st2[32 * kLanes], st3[32 * kLanes];
+  __shared__ uint32_t sc[2][32 * kLanes];
+  __shared__ int32_t first[kMaxEntries + 1];
+  __shared__ int32_t wave_total[4];
+  if (g.status[0] != 0) return;
+  const int tid = threadIdx.x, lane = tid & (kLanes - 1);
+  const int w = __builtin_amdgcn_readfirstlane(tid / kLanes);
+  const int r16 = lane & 15, kb = lane >> 4;
+
+  // Row tiles before every entry: a scan over the groups' sizes.
+  const int entries = g.R * g.per, nt = (a.N + kOut - 1) / kOut;
+  {
+    const int each = (entries + kTileThreads - 1) / kTileThreads;
+    int sum = 0;
+    for (int i = 0; i < each; ++i) {
+      const int e = tid * each + i;
+      if (e >= entries) break;
+      const Span s = group_span(g, e / g.per, e % g.per);
+      const int t = (s.real_end - s.begin + kTile - 1) / kTile;
+      first[e + 1] = t;
+      sum += t;
+    }
+    int incl = sum;
+    for (int k = 1; k < kLanes; k *= 2) {
+      const int o = __shfl_up(incl, k);
+      if (lane >= k) incl += o;
+    }
+    if (lane == kLanes - 1) wave_total[w] = incl;
+    __syncthreads();
+    int before = incl - sum;
+    for (int i = 0; i < w; ++i) before += wave_total[i];
+    for (int i = 0; i < each; ++i) {
+      const int e = tid * each + i;
+      if (e >= entries) break;
+      before += first[e + 1];
+      first[e + 1] = before;
+    }
+    if (tid == 0) first[0] = 0;
+    __syncthreads();
+  }
+  // Consecutive tiles share weights or rows, so each XCD (workgroups go round
+  // the eight) takes one run of them: its L2 serves the sharing.
+  const int total = first[entries] * nt;
+  const int xcd = blockIdx.x & 7, xn = gridDim.x >> 3;
+  const int t_end = (int)((int64_t)total * (xcd + 1) / 8);
+  int t_load = (int)((int64_t)total * xcd / 8) + (int)(blockIdx.x >> 3);
+  if (t_load >= t_end) return;
+
+  const auto find = [&](int t) {
+    const int mt = t / nt;
+    int lo = 0, hi = entries;  // first[lo] <= mt < first[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (first[mid] <= mt)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    Tile o;
+    const int m_tiles = first[lo + 1] - first[lo];
+    const int in = t - first[lo] * nt;
+    const int m = in % m_tiles;
+    const Span sp = group_span(g, lo / g.per, lo % g.per);
+    o.u = uniform(lo / g.per);
+    o.j = uniform(lo % g.per);
+    o.n0 = uniform(in / m_tiles * kOut);
+    o.row0 = uniform(sp.begin + m * kTile);
+    o.rows = uniform(sp.real_end - (sp.begin + m * kTile));
+    o.pad = uniform(m == m_tiles - 1 ? sp.end - sp.real_end : 0);
+    return o;
+  };
+
+  const int blocks = a.K / 32, turns = (blocks + 15) / 16;
+  // Load cursor: its wave's eight fragments (waves 0 and 1 take the weights, 2
+  // and 3 the window rows) as byte offsets of this lane's row and scale block
+  // from two bases, and this thread's two rows of scales.
+  const uint8_t *src_lo, *src_hi, *src_scale[2];
+  uint32_t off[8];
+  const auto point = [&](const Tile& t) {
+    const uint8_t *wq[2], *ws[2];
+    weight_of(g, a.w[0], t.u, t.j, a.N, a.K, &wq[0], &ws[0]);
+    weight_of(g, a.w[Swiglu ? 1 : 0], t.u, t.j, a.N, a.K, &wq[1], &ws[1]);
+    const int64_t base = (int64_t)t.u * g.NvS + t.row0;
+    // Output that row m (0..31) of weight fragment f (0..7, four a wave) is
+    // for; with a gate two gate fragments and the up fragments of the same
+    // outputs alternate.  Row m = 8 q + 4 h + i of the product is register
+    // 4 q + i of the lanes of half h.
+    const auto weight_row = [&](int f, int m) {
+      const int h = (m >> 2) & 1, r = (m >> 3) * 4 + (m & 3);
+      const int n = Swiglu ? (f >> 2) * 64 + h * 32 + (f & 1) * 16 + r
+                           : (f >> 2) * 128 + h * 64 + (f & 3) * 16 + r;
+      return min(t.n0 + n, a.N - 1);
+    };
+    src_lo = w < 2 ? wq[0] : a.xq + base * blocks * 16;
+    src_hi = w < 2 ? wq[1] : src_lo;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int f = w * 8 + i;
+      const int row = w < 2 ? weight_row(f >> 1, (f & 1) * 16 + r16)
+                            : min((f - 16) * 16 + r16, t.rows - 1);
+      off[i] = (uint32_t)row * (uint32_t)(blocks * 16);
+    }
+    const int f = tid >> 4, r = tid & 15;
+    src_scale[0] = ((f >> 2) & 1 ? ws[1] : ws[0]) +
+                   (int64_t)weight_row(f >> 1, (f & 1) * 16 + r) * blocks;
+    src_scale[1] = a.xs + (base + min(tid, t.rows - 1)) * blocks;
+  };
+
+  // Blocks behind the row's end are read from its start: 4-bit codes are all
+  // finite, and the scales 2^-127 of both operands there make what they add
+  // (below 2^-240) vanish in fp32.
+  const auto fill = [&](vec4u* dst, int turn, int step) {
+    const int b = turn * 16 + step * 4 + kb;
+    const uint32_t at = Whole || b < blocks ? 16u * b : 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      load_lds16((i < 4 ? src_lo : src_hi) + (off[i] + at), dst + (w * 8 + i) * kLanes);
+  };
+  // Scales of one turn: 16 bytes of each of the thread's two rows; unless K is
+  // Whole turns, a row's last blocks byte by byte, with 2^-127 behind them.
+  const int scale_at = (tid >> 4) * kLanes + (tid & 15);
+  const auto get_scales = [&](int turn, vec4u(&v)[2]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (Whole || turn * 16 + 16 <= blocks) {
+        __builtin_memcpy(&v[i], src_scale[i] + turn * 16, 16);
+      } else {
+        v[i] = vec4u{0u, 0u, 0u, 0u};
+#pragma unroll 1
+        for (int k = 0; k < 16; ++k) {  // bytes move in from the top
+          const int n = turn * 16 + k;
+          const uint32_t in = n < blocks ? src_scale[i][n] : 0u;
+          v[i].x = v[i].x >> 8 | v[i].y << 24;
+          v[i].y = v[i].y >> 8 | v[i].z << 24;
+          v[i].z = v[i].z >> 8 | v[i].w << 24;
+          v[i].w = v[i].w >> 8 | in << 24;
+        }
+      }
+    }
+  };
+  const auto put_scales = [&](int b, const vec4u(&v)[2]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const vec4u t = transpose_scales(v[i]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sc[b][scale_at + 16 * kLanes * i + 16 * k] = t[k];
+    }
+  };
+
+  // This wave's fragments (32 rows, two blocks of 16): weights (w & 1)*4 ..,
+  // window rows 8 + (w >> 1)*4 ..; a lane holds row lane % 32 and, of the four
+  // scale blocks of a step, 2 * half + lane / 32.
+  vec16f acc[4][4];
+  vec4u fa[8], fb[8];
+  uint32_t sr[2][8], sr_next[2][8];
+  const int in_frag = ((lane >> 4) & 1) * kLanes + (lane >> 5) * 16 + r16;
+  const int wbase = (w & 1) * 8 * kLanes + in_frag, xbase = (16 + (w >> 1) * 8) * kLanes + in_frag;
+  const auto read_scales = [&](int b, uint32_t(&s)[2][8]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[h][i] = sc[b][wbase + i * 2 * kLanes + 32 * h];
+        s[h][4 + i] = sc[b][xbase + i * 2 * kLanes + 32 * h];
+      }
+  };
+
+  Tile cur = find(t_load), next = cur;
+  point(cur);
+  {
+    vec4u v[2];
+    get_scales(0, v);
+    fill(st0, 0, 0);
+    fill(st1, 0, 1);
+    fill(st2, 0, 2);
+    fill(st3, 0, 3);
+    put_scales(0, v);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    fa[i] = st0[wbase + i * 2 * kLanes];
+    fa[4 + i] = st0[xbase + i * 2 * kLanes];
+  }
+  read_scales(0, sr);
+  int buf = 0;
+  bool more = true;  // a turn is left to load
+  while (true) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][k][r] = 0.0f;
+#pragma unroll 1
+    for (int turn = 0; turn < turns; ++turn) {
+      // The turn to load: the next of this tile, or the first of the next
+      // tile; behind the last one it is loaded again, for nothing.
+      int turn_load = turn + 1;
+      if (turn_load == turns) {
+        turn_load = 0;
+        t_load += xn;
+        more = t_load < t_end;
+        if (more) {
+          next = find(t_load);
+          point(next);
+        }
+      }
+      vec4u v[2];
+      get_scales(turn_load, v);
+      // In the middle of a step its second half has been read (by every wave,
+      // behind the barrier), so its buffer is free, and the next step's data,
+      // all but the last two steps' loads (16 of this wave), has landed.
+#define MOON_STEP(S, THIS, NEXT)                                                       \
+  {                                                                                    \
+    wait_lds();                                                                        \
+    half_step<S>(THIS + wbase + 32, THIS + xbase + 32, fa, fb, sr[0], acc);                 \
+    __builtin_amdgcn_sched_barrier(0);                                                 \
+    wait_lds();                                                                        \
+    wait_vm<16>();                                                                     \
+    asm volatile("" ::: "memory");                                                     \
+    __builtin_amdgcn_s_barrier();                                                      \
+    asm volatile("" ::: "memory");                                                     \
+    __builtin_amdgcn_sched_barrier(0);                                                 \
+    fill(THIS, turn_load, S);                                                          \
+    if (S == 2) put_scales(buf ^ 1, v);                                                \
+    if (S == 3) read_scales(buf ^ 1, sr_next);                                         \
+    half_step<S>(NEXT + wbase, NEXT + xbase, fb, fa, sr[1], acc);                     \
+    __builtin_amdgcn_sched_barrier(0);                                                 \
+  }
+      MOON_STEP(0, st0, st1)
+      MOON_STEP(1, st1, st2)
+      MOON_STEP(2, st2, st3)
+      MOON_STEP(3, st3, st0)
+#undef MOON_STEP
+      buf ^= 1;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sr[0][i] = sr_next[0][i];
+        sr[1][i] = sr_next[1][i];
+      }
+    }
+    const int64_t base = (int64_t)cur.u * g.NvS + cur.row0;
+    const int half = lane >> 5, run = kOut / 4;  // outputs a lane holds of a row
+    const int col = cur.n0 + (w & 1) * (kOut / 2) + half * run;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int m = (w >> 1) * 128 + k * 32 + (lane & 31);
+      const bool in = m < cur.rows;
+      const float rw = Swiglu && a.row_w != nullptr && in ? a.row_w[base + m] : 1.0f;
+      uint16_t* const y = a.y + (base + m) * a.N + col;
+#pragma unroll
+      for (int i = 0; i < (Swiglu ? 2 : 4); ++i)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float o[8];
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            o[r] = acc[i][k][8 * q + r];
+            if (Swiglu) o[r] = rw * (o[r] * sigmoid_f32(o[r]) * acc[(i + 2) & 3][k][8 * q + r]);
+          }
+          const vec4u p = {pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
+                           pack_bf16(o[6], o[7])};
+          if (in && col + 16 * i + 8 * q < a.N) *reinterpret_cast<vec4u*>(y + 16 * i + 8 * q) = p;
+        }
+    }
+    zero_rows(a.y, base + cur.rows, cur.pad, a.N, cur.n0, kOut);
+    if (!more) break;
+    cur = next;
+  }
+  wait_vm<0>();  // nothing may land in LDS after the workgroup has left
+}
+
 moon_status check(const ExpertArgs& a, const moon_plan_arrays* plan, int products, Groups* g) {
   const moon_status st = make_groups(plan, g);
   if (st != MOON_OK) return st;
@@ -179,6 +544,18 @@ moon_status check(const ExpertArgs& a, const moon_plan_arrays* plan, int product
 
 template <bool Swiglu>
 moon_status launch(const ExpertArgs& a, const Groups& g, hipStream_t s) {
+  const int64_t rows = (int64_t)g.R * g.N;
+  if (rows >= 96 * (int64_t)g.E && g.R * g.per <= kMaxEntries) {
+    int dev = 0, cus = 256;
+    if (hipGetDevice(&dev) == hipSuccess)
+      (void)hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+    const int wgs = std::max(8, cus / 8 * 8);
+    if (a.K % 512 == 0)
+      hipLaunchKernelGGL((k_expert_tiles<Swiglu, true>), dim3(wgs), dim3(kTileThreads), 0, s, a, g);
+    else
+      hipLaunchKernelGGL((k_expert_tiles<Swiglu, false>), dim3(wgs), dim3(kTileThreads), 0, s, a, g);
+    return hipGetLastError() == hipSuccess ? MOON_OK : MOON_ERR_HIP;
+  }
   const dim3 grid((a.N + 31) / 32, g.R * g.per);
   hipLaunchKernelGGL((k_expert_stream<4, Swiglu>), grid, dim3(256), 0, s, a, g);
   return hipGetLastError() == hipSuccess ? MOON_OK : MOON_ERR_HIP;

@@ -21,6 +21,7 @@ typedef __bf16 vec2bf __attribute__((ext_vector_type(2)));
 struct Groups {
   const int32_t *cu, *zfr, *status;
   int32_t R, E, EB, Eg, B, per, NvS;
+  int32_t N;  // routes per rank (its window's capacity where the caller leaves it out)
 };
 
 struct Span {
@@ -163,6 +164,7 @@ inline moon_status make_groups(const moon_plan_arrays* p, Groups* g) {
   g->Eg = p->E / p->R;
   g->per = g->Eg + p->B;
   g->NvS = p->NvS;
+  g->N = p->N > 0 && p->N < p->NvS ? p->N : p->NvS;
   return MOON_OK;
 }
 
