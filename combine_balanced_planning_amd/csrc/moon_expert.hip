@@ -183,6 +183,15 @@ __device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(0xC07F);
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
+// The thread's index as a value the compiler knows nothing of: what follows
+// from it is worked out where it is used, not kept in registers across the
+// main loop, which needs them all.
+__device__ __forceinline__ int fresh_thread_id() {
+  int t = threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
+}
+
 // One tile of results; every field is the same in all lanes.
 struct Tile {
   int u, j;          // rank and entry
@@ -241,9 +250,11 @@ __device__ __forceinline__ void half_step(const vec4u* wsrc, const vec4u* xsrc, 
 // A workgroup of four waves (one per SIMD) walks tiles of 256 weight rows by
 // 256 window rows; each wave owns 128 by 128 of them (256 accumulators a lane,
 // v_mfma_scale_f32_32x32x64).  K advances by 128 values a step, four steps to a
-// turn of 512.  LDS holds four steps of both operands: global_load_lds writes
-// 16 rows by four scale blocks in lane order, ds_read_b128 takes them out
-// without bank conflicts.  Each step refills the buffer it has just emptied
+// turn of 512.  LDS holds four steps of both operands: a global_load_lds writes
+// 16 rows by four scale blocks in lane order, four lanes a row so that they
+// share its 64 bytes (with a row per lane, 16 lines for 16 lanes, the first
+// cache took twice the time of the products); the blocks of a row are stored
+// swapped by its index, so that ds_read_b128 of 16 rows meets no bank twice.  Each step refills the buffer it has just emptied
 // with the same step of the next turn, which may belong to the next tile: the
 // loads run three steps ahead without a pause at tile borders.  The weight rows
 // of a fragment are dealt so that a lane ends up with 64 neighbouring outputs
@@ -259,7 +270,7 @@ __global__ void __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_
   if (g.status[0] != 0) return;
   const int tid = threadIdx.x, lane = tid & (kLanes - 1);
   const int w = __builtin_amdgcn_readfirstlane(tid / kLanes);
-  const int r16 = lane & 15, kb = lane >> 4;
+  const int chunk = (lane & 3) ^ (lane >> 4);  // scale block that this lane loads
 
   // Row tiles before every entry: a scan over the groups' sizes.
   const int entries = g.R * g.per, nt = (a.N + kOut - 1) / kOut;
@@ -331,6 +342,7 @@ __global__ void __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_
   const uint8_t *src_lo, *src_hi, *src_scale[2];
   uint32_t off[8];
   const auto point = [&](const Tile& t) {
+    const int tid = fresh_thread_id(), r16 = (tid & (kLanes - 1)) >> 2;
     const uint8_t *wq[2], *ws[2];
     weight_of(g, a.w[0], t.u, t.j, a.N, a.K, &wq[0], &ws[0]);
     weight_of(g, a.w[Swiglu ? 1 : 0], t.u, t.j, a.N, a.K, &wq[1], &ws[1]);
@@ -364,7 +376,7 @@ __global__ void __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_
   // finite, and the scales 2^-127 of both operands there make what they add
   // (below 2^-240) vanish in fp32.
   const auto fill = [&](vec4u* dst, int turn, int step) {
-    const int b = turn * 16 + step * 4 + kb;
+    const int b = turn * 16 + step * 4 + chunk;
     const uint32_t at = Whole || b < blocks ? 16u * b : 0u;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -407,15 +419,17 @@ __global__ void __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_
   vec16f acc[4][4];
   vec4u fa[8], fb[8];
   uint32_t sr[2][8], sr_next[2][8];
-  const int in_frag = ((lane >> 4) & 1) * kLanes + (lane >> 5) * 16 + r16;
-  const int wbase = (w & 1) * 8 * kLanes + in_frag, xbase = (16 + (w >> 1) * 8) * kLanes + in_frag;
+  const int wfrag = (w & 1) * 8 * kLanes, xfrag = (16 + (w >> 1) * 8) * kLanes;
+  const int in_block = ((lane >> 4) & 1) * kLanes + (lane & 15) * 4;
+  const int in0 = in_block + ((lane >> 5) ^ ((lane >> 2) & 3)), in1 = in0 ^ 2;
+  const int scale_in = ((lane >> 4) & 1) * kLanes + (lane >> 5) * 16 + (lane & 15);
   const auto read_scales = [&](int b, uint32_t(&s)[2][8]) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        s[h][i] = sc[b][wbase + i * 2 * kLanes + 32 * h];
-        s[h][4 + i] = sc[b][xbase + i * 2 * kLanes + 32 * h];
+        s[h][i] = sc[b][wfrag + scale_in + i * 2 * kLanes + 32 * h];
+        s[h][4 + i] = sc[b][xfrag + scale_in + i * 2 * kLanes + 32 * h];
       }
   };
 
@@ -433,8 +447,8 @@ __global__ void __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    fa[i] = st0[wbase + i * 2 * kLanes];
-    fa[4 + i] = st0[xbase + i * 2 * kLanes];
+    fa[i] = st0[wfrag + in0 + i * 2 * kLanes];
+    fa[4 + i] = st0[xfrag + in0 + i * 2 * kLanes];
   }
   read_scales(0, sr);
   int buf = 0;
@@ -468,7 +482,7 @@ __global__ void __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_
 #define MOON_STEP(S, THIS, NEXT)                                                       \
   {                                                                                    \
     wait_lds();                                                                        \
-    half_step<S>(THIS + wbase + 32, THIS + xbase + 32, fa, fb, sr[0], acc);                 \
+    half_step<S>(THIS + wfrag + in1, THIS + xfrag + in1, fa, fb, sr[0], acc);                 \
     __builtin_amdgcn_sched_barrier(0);                                                 \
     wait_lds();                                                                        \
     wait_vm<16>();                                                                     \
@@ -479,7 +493,7 @@ __global__ void __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_
     fill(THIS, turn_load, S);                                                          \
     if (S == 2) put_scales(buf ^ 1, v);                                                \
     if (S == 3) read_scales(buf ^ 1, sr_next);                                         \
-    half_step<S>(NEXT + wbase, NEXT + xbase, fb, fa, sr[1], acc);                     \
+    half_step<S>(NEXT + wfrag + in0, NEXT + xfrag + in0, fb, fa, sr[1], acc);                     \
     __builtin_amdgcn_sched_barrier(0);                                                 \
   }
       MOON_STEP(0, st0, st1)
@@ -495,6 +509,7 @@ __global__ void __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_
       }
     }
     const int64_t base = (int64_t)cur.u * g.NvS + cur.row0;
+    const int lane = fresh_thread_id() & (kLanes - 1);
     const int half = lane >> 5, run = kOut / 4;  // outputs a lane holds of a row
     const int col = cur.n0 + (w & 1) * (kOut / 2) + half * run;
 #pragma unroll
