@@ -163,15 +163,20 @@ __global__ void __launch_bounds__(256) k_expert_stream(ExpertArgs a, Groups g) {
 
 // ---- many rows per group: tiles of 256 weight rows by 256 window rows ----
 
-constexpr int kTileThreads = 256;
+constexpr int kTileWaves = 8;
+constexpr int kTileThreads = kTileWaves * kLanes;
 constexpr int kTile = 256;
-constexpr int kMaxEntries = 2048;  // of the tile table
+constexpr int kMaxEntries = 1024;  // of the tile table
 
-// 16 bytes per lane from global memory straight into LDS, lane l at dst + 16 l.
-__device__ __forceinline__ void load_lds16(const uint8_t* src, vec4u* dst) {
-  __builtin_amdgcn_global_load_lds(
-      (const __attribute__((address_space(1))) void*)src,
-      (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+// `bytes` bytes from p as a buffer: loads beyond them read nothing and give 0.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint8_t* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, (int)bytes, 0x00027000);
+}
+
+// 16 bytes per lane from a buffer straight into LDS, lane l at dst + 16 l.
+__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t src, uint32_t at, vec4u* dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void*)dst, 16,
+                                           (int)at, 0, 0, 0);
 }
 
 // Waits until at most n vector memory operations of this wave are in flight.
@@ -223,50 +228,50 @@ __device__ __forceinline__ vec16f mfma32(vec4u a, vec4u b, vec16f c, uint32_t sa
                                                          (int)sb);
 }
 
-// Half a step of a wave (64 values): 16 products of its four weight and four
-// row fragments f, while the fragments n of the next half come from LDS.  The
-// schedule puts two reads before each of the first four pairs of products, so
+// Half a step of a wave (64 values): 8 products of its four weight and two row
+// fragments f, while the fragments n of the next half come from LDS.  The
+// schedule puts two reads before each of the first three pairs of products, so
 // they have arrived when the half ends.
 template <int Step>
-__device__ __forceinline__ void half_step(const vec4u* wsrc, const vec4u* xsrc, const vec4u (&f)[8],
-                                          vec4u (&n)[8], const uint32_t (&s)[8],
-                                          vec16f (&acc)[4][4]) {
+__device__ __forceinline__ void half_step(const vec4u* wsrc, const vec4u* xsrc, const vec4u (&f)[6],
+                                          vec4u (&n)[6], const uint32_t (&s)[6],
+                                          vec16f (&acc)[4][2]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) n[i] = wsrc[i * 2 * kLanes];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) n[4 + i] = xsrc[i * 2 * kLanes];
+  for (int i = 0; i < 2; ++i) n[4 + i] = xsrc[i * 2 * kLanes];
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
+  for (int k = 0; k < 2; ++k)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       acc[i][k] = mfma32<Step>(f[i], f[4 + k], acc[i][k], s[i], s[4 + k]);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    if (k < 4) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+  for (int k = 0; k < 4; ++k) {
+    if (k < 3) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
     __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
   }
 }
 
-// A workgroup of four waves (one per SIMD) walks tiles of 256 weight rows by
-// 256 window rows; each wave owns 128 by 128 of them (256 accumulators a lane,
+// A workgroup of eight waves (two per SIMD) walks tiles of 256 weight rows by
+// 256 window rows; each wave owns 128 by 64 of them (128 accumulators a lane,
 // v_mfma_scale_f32_32x32x64).  K advances by 128 values a step, four steps to a
-// turn of 512.  LDS holds four steps of both operands: a global_load_lds writes
-// 16 rows by four scale blocks in lane order, four lanes a row so that they
-// share its 64 bytes (with a row per lane, 16 lines for 16 lanes, the first
-// cache took twice the time of the products); the blocks of a row are stored
-// swapped by its index, so that ds_read_b128 of 16 rows meets no bank twice.  Each step refills the buffer it has just emptied
-// with the same step of the next turn, which may belong to the next tile: the
-// loads run three steps ahead without a pause at tile borders.  The weight rows
-// of a fragment are dealt so that a lane ends up with 64 neighbouring outputs
-// (32 with a gate) of four window rows.
+// turn of 512.  LDS holds four steps of both operands: a load straight into it
+// writes 16 rows by four scale blocks in lane order, four lanes a row so that
+// they share its 64 bytes (with a row per lane, 16 lines for 16 lanes, the
+// first cache took twice the time of the products); the blocks of a row are
+// stored swapped by its index, so that ds_read_b128 of 16 rows meets no bank
+// twice.  Each step refills the buffer it has just emptied with the same step
+// of the next turn, which may belong to the next tile: the loads run three
+// steps ahead without a pause at tile borders.
 template <bool Swiglu, bool Whole>
-__global__ void __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
+__global__ void __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
     k_expert_tiles(ExpertArgs a, Groups g) {
   constexpr int kOut = Swiglu ? kTile / 2 : kTile;  // outputs per tile
   __shared__ vec4u st0[32 * kLanes], st1[32 * kLanes], st2[32 * kLanes], st3[32 * kLanes];
   __shared__ uint32_t sc[2][32 * kLanes];
   __shared__ int32_t first[kMaxEntries + 1];
-  __shared__ int32_t wave_total[4];
+  __shared__ int32_t wave_total[kTileWaves];
+  __shared__ vec4u turned[kTileWaves][kLanes];
   if (g.status[0] != 0) return;
   const int tid = threadIdx.x, lane = tid & (kLanes - 1);
   const int w = __builtin_amdgcn_readfirstlane(tid / kLanes);
@@ -336,128 +341,152 @@ __global__ void __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_
   };
 
   const int blocks = a.K / 32, turns = (blocks + 15) / 16;
-  // Load cursor: its wave's eight fragments (waves 0 and 1 take the weights, 2
-  // and 3 the window rows) as byte offsets of this lane's row and scale block
-  // from two bases, and this thread's two rows of scales.
-  const uint8_t *src_lo, *src_hi, *src_scale[2];
-  uint32_t off[8];
+  // Load cursor: the wave's operand (waves 0 to 3 take the weights, two
+  // fragments each, the others the window rows) and its scales as buffers that
+  // end with the tile's last row, so rows behind it read as zeros.
+  const bool is_w = w < 4;
+  __amdgpu_buffer_rsrc_t src, src_scales;
+  const uint8_t* src_scale;
+  // Output that row m (0..31) of weight fragment f (0..7, four a wave) is for;
+  // with a gate two gate fragments and the up fragments of the same outputs
+  // alternate.  Row m = 8 q + 4 h + i of the product is register 4 q + i of the
+  // lanes of half h.
+  const auto weight_row = [&](int f, int m) {
+    const int h = (m >> 2) & 1, r = (m >> 3) * 4 + (m & 3);
+    return (Swiglu ? (f >> 2) * 64 + (f & 1) * 32 : f * 32) + h * 16 + r;
+  };
+  const uint32_t row_bytes = 16u * blocks;
   const auto point = [&](const Tile& t) {
-    const int tid = fresh_thread_id(), r16 = (tid & (kLanes - 1)) >> 2;
     const uint8_t *wq[2], *ws[2];
     weight_of(g, a.w[0], t.u, t.j, a.N, a.K, &wq[0], &ws[0]);
     weight_of(g, a.w[Swiglu ? 1 : 0], t.u, t.j, a.N, a.K, &wq[1], &ws[1]);
     const int64_t base = (int64_t)t.u * g.NvS + t.row0;
-    // Output that row m (0..31) of weight fragment f (0..7, four a wave) is
-    // for; with a gate two gate fragments and the up fragments of the same
-    // outputs alternate.  Row m = 8 q + 4 h + i of the product is register
-    // 4 q + i of the lanes of half h.
-    const auto weight_row = [&](int f, int m) {
-      const int h = (m >> 2) & 1, r = (m >> 3) * 4 + (m & 3);
-      const int n = Swiglu ? (f >> 2) * 64 + h * 32 + (f & 1) * 16 + r
-                           : (f >> 2) * 128 + h * 64 + (f & 3) * 16 + r;
-      return min(t.n0 + n, a.N - 1);
-    };
-    src_lo = w < 2 ? wq[0] : a.xq + base * blocks * 16;
-    src_hi = w < 2 ? wq[1] : src_lo;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int f = w * 8 + i;
-      const int row = w < 2 ? weight_row(f >> 1, (f & 1) * 16 + r16)
-                            : min((f - 16) * 16 + r16, t.rows - 1);
-      off[i] = (uint32_t)row * (uint32_t)(blocks * 16);
+    const int nr = min(a.N - t.n0, kOut), mr = min(t.rows, kTile);
+    const uint32_t rows = is_w ? nr : mr;
+    const uint8_t* const q = Swiglu && (w & 1) ? wq[1] : wq[0];
+    const uint8_t* const sq = Swiglu && (w & 1) ? ws[1] : ws[0];
+    src = buffer(is_w ? q + (int64_t)t.n0 * row_bytes : a.xq + base * row_bytes, rows * row_bytes);
+    if (Whole) {
+      src_scales = buffer(is_w ? sq + (int64_t)t.n0 * blocks : a.xs + base * blocks, rows * blocks);
+    } else {  // a row per thread, in the order of the fragments
+      const int tid = fresh_thread_id(), f = (tid >> 4) & 15, r = tid & 15;
+      src_scale = is_w ? ((f >> 2) & 1 ? ws[1] : ws[0]) +
+                             (int64_t)(t.n0 + min(weight_row(f >> 1, (f & 1) * 16 + r), nr - 1)) * blocks
+                       : a.xs + (base + min(tid - kTile, mr - 1)) * blocks;
     }
-    const int f = tid >> 4, r = tid & 15;
-    src_scale[0] = ((f >> 2) & 1 ? ws[1] : ws[0]) +
-                   (int64_t)weight_row(f >> 1, (f & 1) * 16 + r) * blocks;
-    src_scale[1] = a.xs + (base + min(tid, t.rows - 1)) * blocks;
   };
 
-  // Blocks behind the row's end are read from its start: 4-bit codes are all
-  // finite, and the scales 2^-127 of both operands there make what they add
-  // (below 2^-240) vanish in fp32.
+  // Codes of one step.  Blocks behind a row's end are those of the next row (or
+  // zeros): 4-bit codes are all finite, and the scales 2^-127 of both operands
+  // there make what they add (below 2^-240) vanish in fp32.
+  const int r16 = lane >> 2;
+  const uint32_t code_at = (is_w ? weight_row(w * 2, r16) : (w - 4) * 64 + r16) * row_bytes +
+                           16 * chunk;
   const auto fill = [&](vec4u* dst, int turn, int step) {
-    const int b = turn * 16 + step * 4 + chunk;
-    const uint32_t at = Whole || b < blocks ? 16u * b : 0u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      load_lds16((i < 4 ? src_lo : src_hi) + (off[i] + at), dst + (w * 8 + i) * kLanes);
+    for (int i = 0; i < 4; ++i) {
+      // rows of block i, relative to the first's
+      const int rows = is_w ? (i >> 1) * 32 + (i & 1) * 8 : i * 16;
+      load_lds16(src, code_at + (rows * row_bytes + turn * 256 + step * 64),
+                 dst + (w * 4 + i) * kLanes);
+    }
   };
-  // Scales of one turn: 16 bytes of each of the thread's two rows; unless K is
-  // Whole turns, a row's last blocks byte by byte, with 2^-127 behind them.
+  // Scales of one turn: 16 bytes of the thread's row; unless K is Whole turns,
+  // a row's last blocks byte by byte, with 2^-127 behind them.
   const int scale_at = (tid >> 4) * kLanes + (tid & 15);
-  const auto get_scales = [&](int turn, vec4u(&v)[2]) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (Whole || turn * 16 + 16 <= blocks) {
-        __builtin_memcpy(&v[i], src_scale[i] + turn * 16, 16);
-      } else {
-        v[i] = vec4u{0u, 0u, 0u, 0u};
+  const auto get_scales = [&](int turn) {
+    vec4u v;
+    if (turn * 16 + 16 <= blocks) {
+      __builtin_memcpy(&v, src_scale + turn * 16, 16);
+    } else {
+      v = vec4u{0u, 0u, 0u, 0u};
 #pragma unroll 1
-        for (int k = 0; k < 16; ++k) {  // bytes move in from the top
-          const int n = turn * 16 + k;
-          const uint32_t in = n < blocks ? src_scale[i][n] : 0u;
-          v[i].x = v[i].x >> 8 | v[i].y << 24;
-          v[i].y = v[i].y >> 8 | v[i].z << 24;
-          v[i].z = v[i].z >> 8 | v[i].w << 24;
-          v[i].w = v[i].w >> 8 | in << 24;
-        }
+      for (int k = 0; k < 16; ++k) {  // bytes move in from the top
+        const int n = turn * 16 + k;
+        const uint32_t in = n < blocks ? src_scale[n] : 0u;
+        v.x = v.x >> 8 | v.y << 24;
+        v.y = v.y >> 8 | v.z << 24;
+        v.z = v.z >> 8 | v.w << 24;
+        v.w = v.w >> 8 | in << 24;
       }
     }
+    return v;
   };
-  const auto put_scales = [&](int b, const vec4u(&v)[2]) {
+  const auto put_scales = [&](int b, vec4u v) {
+    const vec4u t = transpose_scales(v);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const vec4u t = transpose_scales(v[i]);
+    for (int k = 0; k < 4; ++k) sc[b][scale_at + 16 * k] = t[k];
+  };
+
+  // Scales of whole turns, two of them (32 bytes of a row) at a time straight
+  // into LDS, as they lie in memory: two lanes a row, 512 rows.
+  vec4u* const raw = reinterpret_cast<vec4u*>(&sc[0][0]);
+  const uint32_t scales_at = (is_w ? weight_row(w * 2, lane >> 1) : (w - 4) * 64 + (lane >> 1)) *
+                                 blocks + 16 * (lane & 1);
+  const auto fill_scales = [&](int turn) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) sc[b][scale_at + 16 * kLanes * i + 16 * k] = t[k];
-    }
+    for (int i = 0; i < 2; ++i)
+      load_lds16(src_scales, scales_at + (i * 32 * blocks + turn * 16), raw + (w * 2 + i) * kLanes);
   };
 
   // This wave's fragments (32 rows, two blocks of 16): weights (w & 1)*4 ..,
-  // window rows 8 + (w >> 1)*4 ..; a lane holds row lane % 32 and, of the four
+  // window rows 8 + (w >> 1)*2 ..; a lane holds row lane % 32 and, of the four
   // scale blocks of a step, 2 * half + lane / 32.
-  vec16f acc[4][4];
-  vec4u fa[8], fb[8];
-  uint32_t sr[2][8], sr_next[2][8];
-  const int wfrag = (w & 1) * 8 * kLanes, xfrag = (16 + (w >> 1) * 8) * kLanes;
+  vec16f acc[4][2];
+  vec4u fa[6], fb[6];
+  uint32_t sr[2][6], sr_next[2][6];
+  const int wfrag = (w & 1) * 8 * kLanes, xfrag = (16 + (w >> 1) * 4) * kLanes;
   const int in_block = ((lane >> 4) & 1) * kLanes + (lane & 15) * 4;
   const int in0 = in_block + ((lane >> 5) ^ ((lane >> 2) & 3)), in1 = in0 ^ 2;
   const int scale_in = ((lane >> 4) & 1) * kLanes + (lane >> 5) * 16 + (lane & 15);
-  const auto read_scales = [&](int b, uint32_t(&s)[2][8]) {
+  // bytes h and 2 + h, the blocks of this half of the lanes, of two words
+  const uint32_t pick = 0x06020400u + 0x01010101u * (lane >> 5);
+  const auto read_scales = [&](int b, int turn, uint32_t(&s)[2][6]) {
+    if (Whole) {
+#pragma unroll
+      for (int i = 0; i < 6; ++i) {
+        const vec4u d = raw[((i < 4 ? wfrag : xfrag) >> 1) + (i & 3) * kLanes +
+                            (lane & 31) * 2 + (turn & 1)];
+        const uint32_t lo = __builtin_amdgcn_perm(d.y, d.x, pick);
+        const uint32_t hi = __builtin_amdgcn_perm(d.w, d.z, pick);
+        s[0][i] = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+        s[1][i] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);
+      }
+      return;
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s[h][i] = sc[b][wfrag + scale_in + i * 2 * kLanes + 32 * h];
-        s[h][4 + i] = sc[b][xfrag + scale_in + i * 2 * kLanes + 32 * h];
-      }
+      for (int i = 0; i < 6; ++i)
+        s[h][i] = sc[b][(i < 4 ? wfrag : xfrag) + scale_in + (i & 3) * 2 * kLanes + 32 * h];
   };
 
   Tile cur = find(t_load), next = cur;
   point(cur);
   {
-    vec4u v[2];
-    get_scales(0, v);
+    vec4u v = {};
+    if (Whole)
+      fill_scales(0);
+    else
+      v = get_scales(0);
     fill(st0, 0, 0);
     fill(st1, 0, 1);
     fill(st2, 0, 2);
     fill(st3, 0, 3);
-    put_scales(0, v);
+    if (!Whole) put_scales(0, v);
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    fa[i] = st0[wfrag + in0 + i * 2 * kLanes];
-    fa[4 + i] = st0[xfrag + in0 + i * 2 * kLanes];
-  }
-  read_scales(0, sr);
+  for (int i = 0; i < 6; ++i)
+    fa[i] = st0[(i < 4 ? wfrag : xfrag) + in0 + (i & 3) * 2 * kLanes];
+  read_scales(0, 0, sr);
   int buf = 0;
   bool more = true;  // a turn is left to load
   while (true) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][k][r] = 0.0f;
 #pragma unroll 1
@@ -474,25 +503,26 @@ __global__ void __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_
           point(next);
         }
       }
-      vec4u v[2];
-      get_scales(turn_load, v);
+      vec4u v = {};
+      if (!Whole) v = get_scales(turn_load);
       // In the middle of a step its second half has been read (by every wave,
       // behind the barrier), so its buffer is free, and the next step's data,
-      // all but the last two steps' loads (16 of this wave), has landed.
+      // all but the last two steps' loads (8 of this wave), has landed.
 #define MOON_STEP(S, THIS, NEXT)                                                       \
   {                                                                                    \
     wait_lds();                                                                        \
     half_step<S>(THIS + wfrag + in1, THIS + xfrag + in1, fa, fb, sr[0], acc);                 \
     __builtin_amdgcn_sched_barrier(0);                                                 \
     wait_lds();                                                                        \
-    wait_vm<16>();                                                                     \
+    wait_vm<8>();                                                                      \
     asm volatile("" ::: "memory");                                                     \
     __builtin_amdgcn_s_barrier();                                                      \
     asm volatile("" ::: "memory");                                                     \
     __builtin_amdgcn_sched_barrier(0);                                                 \
+    if (Whole && S == 0 && (turn_load & 1) == 0) fill_scales(turn_load);               \
     fill(THIS, turn_load, S);                                                          \
-    if (S == 2) put_scales(buf ^ 1, v);                                                \
-    if (S == 3) read_scales(buf ^ 1, sr_next);                                         \
+    if (!Whole && S == 2) put_scales(buf ^ 1, v);                                      \
+    if (S == 3) read_scales(buf ^ 1, turn_load, sr_next);                              \
     half_step<S>(NEXT + wfrag + in0, NEXT + xfrag + in0, fb, fa, sr[1], acc);                     \
     __builtin_amdgcn_sched_barrier(0);                                                 \
   }
@@ -503,23 +533,28 @@ __global__ void __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_
 #undef MOON_STEP
       buf ^= 1;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 6; ++i) {
         sr[0][i] = sr_next[0][i];
         sr[1][i] = sr_next[1][i];
       }
     }
     const int64_t base = (int64_t)cur.u * g.NvS + cur.row0;
+    // A lane holds 16 neighbouring outputs of one row per fragment; through LDS,
+    // 16 rows at a time, four lanes get a row's 64 bytes, so that a store writes
+    // whole segments.
     const int lane = fresh_thread_id() & (kLanes - 1);
-    const int half = lane >> 5, run = kOut / 4;  // outputs a lane holds of a row
-    const int col = cur.n0 + (w & 1) * (kOut / 2) + half * run;
+    const int row = lane & 31, col = cur.n0 + (w & 1) * (kOut / 2);
+    vec4u* const put = &turned[w][(lane & 15) * 4];
+    const int swap = (lane >> 2) & 3, half = lane >> 5;
+    const int out_row = lane >> 2, out_col = ((lane & 3) ^ (lane >> 4)) * 8;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int m = (w >> 1) * 128 + k * 32 + (lane & 31);
-      const bool in = m < cur.rows;
-      const float rw = Swiglu && a.row_w != nullptr && in ? a.row_w[base + m] : 1.0f;
-      uint16_t* const y = a.y + (base + m) * a.N + col;
+    for (int k = 0; k < 2; ++k) {
+      const int m = (w >> 1) * 64 + k * 32;
+      const float rw = Swiglu && a.row_w != nullptr && m + row < cur.rows
+                           ? a.row_w[base + m + row] : 1.0f;
 #pragma unroll
-      for (int i = 0; i < (Swiglu ? 2 : 4); ++i)
+      for (int i = 0; i < (Swiglu ? 2 : 4); ++i) {
+        vec4u v[2];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           float o[8];
@@ -528,10 +563,24 @@ __global__ void __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_
             o[r] = acc[i][k][8 * q + r];
             if (Swiglu) o[r] = rw * (o[r] * sigmoid_f32(o[r]) * acc[(i + 2) & 3][k][8 * q + r]);
           }
-          const vec4u p = {pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
-                           pack_bf16(o[6], o[7])};
-          if (in && col + 16 * i + 8 * q < a.N) *reinterpret_cast<vec4u*>(y + 16 * i + 8 * q) = p;
+          v[q] = vec4u{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
+                       pack_bf16(o[6], o[7])};
         }
+        const int c = col + 32 * i + out_col;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (((lane >> 4) & 1) == j) {
+            put[(2 * half) ^ swap] = v[0];
+            put[(2 * half + 1) ^ swap] = v[1];
+          }
+          wave_lds_sync();
+          const vec4u p = turned[w][lane];
+          wave_lds_sync();
+          const int r = m + 16 * j + out_row;
+          if (r < cur.rows && c < a.N) *reinterpret_cast<vec4u*>(a.y + (base + r) * a.N + c) = p;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
     zero_rows(a.y, base + cur.rows, cur.pad, a.N, cur.n0, kOut);
     if (!more) break;
