@@ -249,6 +249,7 @@ __device__ __forceinline__ void half_step(const vec4u* wsrc, const vec4u* xsrc, 
   for (int k = 0; k < 4; ++k) {
     if (k < 3) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
     __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+    __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
   }
 }
 
