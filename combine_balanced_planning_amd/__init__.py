@@ -331,20 +331,25 @@ def moon_reduce_grad(ctx, plan, grads, slot_grads, stream=None):
 _DTYPES = {torch.float32: MOON_DTYPE_F32, torch.bfloat16: MOON_DTYPE_BF16}
 
 
-def _one_device(tensors):
-    """The device index that every given tensor (None skipped) lives on."""
-    dev = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a contiguous CUDA tensor")
-        if dev is None:
-            dev = t.device.index
-        elif t.device.index != dev:
-            raise ValueError(f"{name} is on cuda:{t.device.index}, the call's other tensors on "
-                             f"cuda:{dev}")
+def _device_of(t, name):
+    """Device index of a call's first tensor."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
     return dev
+
+
+def _addr(t, dtype, numel, name, dev):
+    """Device address of a tensor after the checks of _ptr, on device `dev`."""
+    if t.dtype is not dtype or t.numel() != numel or t.get_device() != dev or \
+            not t.is_contiguous():
+        _ptr(t, dtype, numel, name)
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{dev}")
+    return t.data_ptr()
+
+
+def _opt(t, dtype, numel, name, dev):
+    return None if t is None else _addr(t, dtype, numel, name, dev)
 
 
 def _dtype_code(t, name):
@@ -357,38 +362,37 @@ def _call(dev, fn, *args, stream=None):
     """Calls the library with `dev` current (switching to it and back if it is not)."""
     f = getattr(_lib, fn)
     if torch.cuda.current_device() == dev:
-        _check(f(*args, _stream(stream)), fn)
+        st = f(*args, (stream or torch.cuda.current_stream()).cuda_stream)
     else:
         with torch.cuda.device(dev):
-            _check(f(*args, _stream(stream)), fn)
+            st = f(*args, (stream or torch.cuda.current_stream()).cuda_stream)
+    if st != MOON_OK:
+        raise MoonError(st, fn)
 
 
-def _groups(plan, rows, tensors):
-    """(moon_plan_arrays, device) of a Plan or a dict of plan arrays, for
+def _groups(plan, rows, dev):
+    """moon_plan_arrays of a Plan or a dict of plan arrays on device `dev`, for
     window tensors of `rows` rows."""
-    dev = _one_device(tensors)
     if isinstance(plan, Plan):
         pa = moon_plan_view(plan)
         if plan.ctx.device != dev:
             raise ValueError(f"the plan is on cuda:{plan.ctx.device}, the tensors on cuda:{dev}")
     else:
-        cu, etc = plan["cu_seqlens"], plan["experts_to_copy"]
-        if cu.dim() != 2 or etc.dim() != 2 or etc.shape[0] != cu.shape[0] or \
-                cu.shape[1] <= etc.shape[1]:
+        cu, etc, dst = plan["cu_seqlens"], plan["experts_to_copy"], plan.get("dst")
+        cs, es = cu.shape, etc.shape
+        if len(cs) != 2 or len(es) != 2 or es[0] != cs[0] or cs[1] <= es[1] or es[1] < 1:
             raise ValueError("cu_seqlens must be [R, E+B] and experts_to_copy [R, B]")
+        R, EB = cs
         pa = moon_plan_arrays()
-        pa.R, pa.B = cu.shape[0], etc.shape[1]
-        pa.E = cu.shape[1] - pa.B
-        pa.NvS = rows // pa.R
-        pa.N = plan["dst"].numel() // pa.R if "dst" in plan else 0
-        for k, n in (("cu_seqlens", cu.numel()), ("zero_fill_ranges", 2 * cu.numel()),
-                     ("status", 1)):
-            setattr(pa, k, _ptr(plan[k], torch.int32, n, k))
-            if plan[k].device.index != dev:
-                raise ValueError(f"{k} is on {plan[k].device}, the tensors on cuda:{dev}")
+        pa.R, pa.B, pa.E, pa.NvS = R, es[1], EB - es[1], rows // R
+        pa.N = dst.numel() // R if dst is not None else 0
+        pa.cu_seqlens = _addr(cu, torch.int32, R * EB, "cu_seqlens", dev)
+        pa.zero_fill_ranges = _addr(plan["zero_fill_ranges"], torch.int32, 2 * R * EB,
+                                    "zero_fill_ranges", dev)
+        pa.status = _addr(plan["status"], torch.int32, 1, "status", dev)
     if rows != pa.R * pa.NvS:
         raise ValueError(f"window tensors must have R*NvS = {pa.R * pa.NvS} rows, got {rows}")
-    return pa, dev
+    return pa
 
 
 def _route_config(logits, K, flags, scale, loss_coef):
@@ -398,12 +402,12 @@ def _route_config(logits, K, flags, scale, loss_coef):
     return moon_route_config(R, S, E, K, _dtype_code(logits, "logits"), flags, scale, loss_coef)
 
 
-def _flags8(valid, n):
+def _flags8(valid, n, dev):
     if valid is None:
         return None
     if valid.dtype not in (torch.bool, torch.uint8):
         raise ValueError(f"valid must be torch.bool or torch.uint8, got {valid.dtype}")
-    return _ptr(valid, valid.dtype, n, "valid")
+    return _addr(valid, valid.dtype, n, "valid", dev)
 
 
 def moon_route(logits, topk, weights, flags=0, scale=1.0, bias=None, valid=None,
@@ -413,31 +417,26 @@ def moon_route(logits, topk, weights, flags=0, scale=1.0, bias=None, valid=None,
     [R, S, K] int32 and weights [R, S, K] float32; the optional outputs are
     described at moon_route in include/moon.h.  workspace: a uint8 tensor of at
     least moon_route_workspace(...) bytes; allocated for the call when None."""
-    if topk.dim() != 3 or tuple(topk.shape[:2]) != tuple(logits.shape[:2]):
+    if topk.dim() != 3 or topk.shape[:2] != logits.shape[:2]:
         raise ValueError(f"topk must be [R, S, K], got {tuple(topk.shape)}")
     cfg = _route_config(logits, topk.shape[2], flags, scale, loss_coef)
     R, S, E, K = cfg.R, cfg.S, cfg.E, cfg.K
-    dev = _one_device(dict(logits=logits, topk=topk, weights=weights, bias=bias, valid=valid,
-                           tokens_per_expert=tokens_per_expert, valid_tokens=valid_tokens,
-                           prob_sums=prob_sums, loss=loss, workspace=workspace))
-    if workspace is None and not (tokens_per_expert is None and valid_tokens is None and
-                                  prob_sums is None and loss is None):
+    dev, i32, f32 = _device_of(logits, "logits"), torch.int32, torch.float32
+    if workspace is None and S > 256 and not (tokens_per_expert is None and valid_tokens is None
+                                              and prob_sums is None and loss is None):
         n = moon_route_workspace(R, S, E, K)
         if n > 0:
             workspace = torch.empty(n, dtype=torch.uint8, device=logits.device)
             if stream is not None:
                 workspace.record_stream(stream)
-    _call(dev, "moon_route", ctypes.byref(cfg), _ptr(logits, logits.dtype, R * S * E, "logits"),
-          _ptr(bias, torch.float32, E, "bias", optional=True), _flags8(valid, R * S),
-          _ptr(topk, torch.int32, R * S * K, "topk"),
-          _ptr(weights, torch.float32, R * S * K, "weights"),
-          _ptr(tokens_per_expert, torch.int32, R * E, "tokens_per_expert", optional=True),
-          _ptr(valid_tokens, torch.int32, R, "valid_tokens", optional=True),
-          _ptr(prob_sums, torch.float32, R * E, "prob_sums", optional=True),
-          _ptr(loss, torch.float32, R, "loss", optional=True),
-          None if workspace is None else _ptr(workspace, torch.uint8, workspace.numel(),
-                                              "workspace"),
-          0 if workspace is None else workspace.numel(), stream=stream)
+    ws_bytes = 0 if workspace is None else workspace.numel()
+    _call(dev, "moon_route", ctypes.byref(cfg), _addr(logits, logits.dtype, R * S * E, "logits", dev),
+          _opt(bias, f32, E, "bias", dev), _flags8(valid, R * S, dev),
+          _addr(topk, i32, R * S * K, "topk", dev), _addr(weights, f32, R * S * K, "weights", dev),
+          _opt(tokens_per_expert, i32, R * E, "tokens_per_expert", dev),
+          _opt(valid_tokens, i32, R, "valid_tokens", dev),
+          _opt(prob_sums, f32, R * E, "prob_sums", dev), _opt(loss, f32, R, "loss", dev),
+          _opt(workspace, torch.uint8, ws_bytes, "workspace", dev), ws_bytes, stream=stream)
 
 
 def moon_route_workspace(R, S, E, K):
@@ -453,21 +452,18 @@ def moon_route_backward(logits, topk, d_logits, flags=0, scale=1.0, valid=None, 
                         stream=None):
     """Gradient of moon_route to d_logits (the shape and dtype of logits) from
     d_weights [R, S, K] and d_loss [R], either of which may be None."""
-    if topk.dim() != 3 or tuple(topk.shape[:2]) != tuple(logits.shape[:2]):
+    if topk.dim() != 3 or topk.shape[:2] != logits.shape[:2]:
         raise ValueError(f"topk must be [R, S, K], got {tuple(topk.shape)}")
     cfg = _route_config(logits, topk.shape[2], flags, scale, loss_coef)
     R, S, E, K = cfg.R, cfg.S, cfg.E, cfg.K
-    dev = _one_device(dict(logits=logits, topk=topk, d_logits=d_logits, valid=valid,
-                           d_weights=d_weights, tokens_per_expert=tokens_per_expert,
-                           valid_tokens=valid_tokens, d_loss=d_loss))
+    dev, i32, f32 = _device_of(logits, "logits"), torch.int32, torch.float32
     _call(dev, "moon_route_backward", ctypes.byref(cfg),
-          _ptr(logits, logits.dtype, R * S * E, "logits"), _flags8(valid, R * S),
-          _ptr(topk, torch.int32, R * S * K, "topk"),
-          _ptr(d_weights, torch.float32, R * S * K, "d_weights", optional=True),
-          _ptr(tokens_per_expert, torch.int32, R * E, "tokens_per_expert", optional=True),
-          _ptr(valid_tokens, torch.int32, R, "valid_tokens", optional=True),
-          _ptr(d_loss, torch.float32, R, "d_loss", optional=True),
-          _ptr(d_logits, logits.dtype, R * S * E, "d_logits"), stream=stream)
+          _addr(logits, logits.dtype, R * S * E, "logits", dev), _flags8(valid, R * S, dev),
+          _addr(topk, i32, R * S * K, "topk", dev),
+          _opt(d_weights, f32, R * S * K, "d_weights", dev),
+          _opt(tokens_per_expert, i32, R * E, "tokens_per_expert", dev),
+          _opt(valid_tokens, i32, R, "valid_tokens", dev), _opt(d_loss, f32, R, "d_loss", dev),
+          _addr(d_logits, logits.dtype, R * S * E, "d_logits", dev), stream=stream)
 
 
 def _mx4_call(fn, x, q, scales, plan, stream):
@@ -475,16 +471,16 @@ def _mx4_call(fn, x, q, scales, plan, stream):
         raise ValueError("values must be [rows, cols]")
     cols = x.shape[-1]
     rows = x.numel() // cols if cols else 0
-    t = dict(values=x, q=q, scales=scales)
-    pa, dev = _groups(plan, rows, t) if plan is not None else (None, _one_device(t))
-    px = _ptr(x, x.dtype, rows * cols, "values")
-    pq = _ptr(q, torch.uint8, rows * (cols // 2), "q")
-    ps = _ptr(scales, torch.uint8, rows * (cols // 32), "scales")
-    code, pp = _dtype_code(x, "values"), None if pa is None else ctypes.byref(pa)
+    dev = _device_of(x, "values")
+    pa = None if plan is None else ctypes.byref(_groups(plan, rows, dev))
+    px = _addr(x, x.dtype, rows * cols, "values", dev)
+    pq = _addr(q, torch.uint8, rows * (cols // 2), "q", dev)
+    ps = _addr(scales, torch.uint8, rows * (cols // 32), "scales", dev)
+    code = _dtype_code(x, "values")
     if fn == "moon_mx4_quantize":
-        _call(dev, fn, px, code, rows, cols, pp, pq, ps, stream=stream)
+        _call(dev, fn, px, code, rows, cols, pa, pq, ps, stream=stream)
     else:
-        _call(dev, fn, pq, ps, rows, cols, pp, code, px, stream=stream)
+        _call(dev, fn, pq, ps, rows, cols, pa, code, px, stream=stream)
 
 
 def moon_mx4_quantize(x, q, scales, plan=None, stream=None):
@@ -498,14 +494,14 @@ def moon_mx4_dequantize(q, scales, y, plan=None, stream=None):
     _mx4_call("moon_mx4_dequantize", y, q, scales, plan, stream)
 
 
-def _mx4_weight(pa, w, N, K, name):
+def _mx4_weight(pa, w, N, K, name, dev):
     """moon_mx4_weight of (expert codes, expert scales, slot codes, slot scales)."""
     eq, es, sq, ss = w
-    E, RB = pa.E, pa.R * pa.B
-    return moon_mx4_weight(_ptr(eq, torch.uint8, E * N * (K // 2), f"{name} expert codes"),
-                           _ptr(es, torch.uint8, E * N * (K // 32), f"{name} expert scales"),
-                           _ptr(sq, torch.uint8, RB * N * (K // 2), f"{name} slot codes"),
-                           _ptr(ss, torch.uint8, RB * N * (K // 32), f"{name} slot scales"))
+    u8, E, RB = torch.uint8, pa.E, pa.R * pa.B
+    return moon_mx4_weight(_addr(eq, u8, E * N * (K // 2), f"{name} expert codes", dev),
+                           _addr(es, u8, E * N * (K // 32), f"{name} expert scales", dev),
+                           _addr(sq, u8, RB * N * (K // 2), f"{name} slot codes", dev),
+                           _addr(ss, u8, RB * N * (K // 32), f"{name} slot scales", dev))
 
 
 def _rows_of(t, name):
@@ -519,31 +515,28 @@ def moon_expert_gemm_mx4(plan, xq, xs, weight, y, stream=None):
     weights of their groups; weight = (expert_q [E, N, K/2], expert_scales
     [E, N, K/32], slot_q [R, B, N, K/2], slot_scales [R, B, N, K/32])."""
     rows, half = _rows_of(xq, "xq")
-    N, K = _rows_of(y, "y")[1], 2 * half
-    pa, dev = _groups(plan, rows, dict(xq=xq, xs=xs, y=y, expert_q=weight[0],
-                                       expert_scales=weight[1], slot_q=weight[2],
-                                       slot_scales=weight[3]))
-    w = _mx4_weight(pa, weight, N, K, "weight")
+    N, K, dev = _rows_of(y, "y")[1], 2 * half, _device_of(xq, "xq")
+    pa = _groups(plan, rows, dev)
+    w = _mx4_weight(pa, weight, N, K, "weight", dev)
     _call(dev, "moon_expert_gemm_mx4", ctypes.byref(pa),
-          _ptr(xq, torch.uint8, rows * half, "xq"), _ptr(xs, torch.uint8, rows * (K // 32), "xs"),
-          K, ctypes.byref(w), N, _ptr(y, torch.bfloat16, rows * N, "y"), stream=stream)
+          _addr(xq, torch.uint8, rows * half, "xq", dev),
+          _addr(xs, torch.uint8, rows * (K // 32), "xs", dev), K, ctypes.byref(w), N,
+          _addr(y, torch.bfloat16, rows * N, "y", dev), stream=stream)
 
 
 def moon_expert_swiglu_mx4(plan, xq, xs, gate, up, h, row_weights=None, stream=None):
     """h [R*NvS, F] bfloat16: the gated activation of two such products; gate
     and up as the weight of moon_expert_gemm_mx4, row_weights [R*NvS] float32."""
     rows, half = _rows_of(xq, "xq")
-    F, K = _rows_of(h, "h")[1], 2 * half
-    t = dict(xq=xq, xs=xs, h=h, row_weights=row_weights)
-    for name, w in (("gate", gate), ("up", up)):
-        t.update({f"{name}[{i}]": x for i, x in enumerate(w)})
-    pa, dev = _groups(plan, rows, t)
-    wg, wu = _mx4_weight(pa, gate, F, K, "gate"), _mx4_weight(pa, up, F, K, "up")
+    F, K, dev = _rows_of(h, "h")[1], 2 * half, _device_of(xq, "xq")
+    pa = _groups(plan, rows, dev)
+    wg = _mx4_weight(pa, gate, F, K, "gate", dev)
+    wu = _mx4_weight(pa, up, F, K, "up", dev)
     _call(dev, "moon_expert_swiglu_mx4", ctypes.byref(pa),
-          _ptr(xq, torch.uint8, rows * half, "xq"), _ptr(xs, torch.uint8, rows * (K // 32), "xs"),
-          K, ctypes.byref(wg), ctypes.byref(wu), F,
-          _ptr(row_weights, torch.float32, rows, "row_weights", optional=True),
-          _ptr(h, torch.bfloat16, rows * F, "h"), stream=stream)
+          _addr(xq, torch.uint8, rows * half, "xq", dev),
+          _addr(xs, torch.uint8, rows * (K // 32), "xs", dev), K, ctypes.byref(wg),
+          ctypes.byref(wu), F, _opt(row_weights, torch.float32, rows, "row_weights", dev),
+          _addr(h, torch.bfloat16, rows * F, "h", dev), stream=stream)
 
 
 def moon_swiglu_save8(plan, gate_up, h, saved, saved_scales, row_weights=None, stream=None):
@@ -551,14 +544,15 @@ def moon_swiglu_save8(plan, gate_up, h, saved, saved_scales, row_weights=None, s
     both bfloat16, keeping gate_up in 8 bits: saved [R*NvS, 2F] and
     saved_scales [R*NvS, 2F/32], uint8."""
     rows, F = _rows_of(h, "h")
-    pa, dev = _groups(plan, rows, dict(gate_up=gate_up, h=h, saved=saved,
-                                       saved_scales=saved_scales, row_weights=row_weights))
+    dev = _device_of(h, "h")
+    pa = _groups(plan, rows, dev)
     _call(dev, "moon_swiglu_save8", ctypes.byref(pa),
-          _ptr(gate_up, torch.bfloat16, rows * 2 * F, "gate_up"),
-          _ptr(row_weights, torch.float32, rows, "row_weights", optional=True), F,
-          _ptr(h, torch.bfloat16, rows * F, "h"),
-          _ptr(saved, torch.uint8, rows * 2 * F, "saved"),
-          _ptr(saved_scales, torch.uint8, rows * (2 * F // 32), "saved_scales"), stream=stream)
+          _addr(gate_up, torch.bfloat16, rows * 2 * F, "gate_up", dev),
+          _opt(row_weights, torch.float32, rows, "row_weights", dev), F,
+          _addr(h, torch.bfloat16, rows * F, "h", dev),
+          _addr(saved, torch.uint8, rows * 2 * F, "saved", dev),
+          _addr(saved_scales, torch.uint8, rows * (2 * F // 32), "saved_scales", dev),
+          stream=stream)
 
 
 def moon_swiglu_grad8(plan, dh, saved, saved_scales, d_gate_up, row_weights=None,
@@ -566,16 +560,15 @@ def moon_swiglu_grad8(plan, dh, saved, saved_scales, d_gate_up, row_weights=None
     """d_gate_up [R*NvS, 2F] bfloat16 and d_row_weights [R*NvS] float32
     (optional) from dh [R*NvS, F] and what moon_swiglu_save8 kept."""
     rows, F = _rows_of(dh, "dh")
-    pa, dev = _groups(plan, rows, dict(dh=dh, saved=saved, saved_scales=saved_scales,
-                                       d_gate_up=d_gate_up, row_weights=row_weights,
-                                       d_row_weights=d_row_weights))
+    dev = _device_of(dh, "dh")
+    pa = _groups(plan, rows, dev)
     _call(dev, "moon_swiglu_grad8", ctypes.byref(pa),
-          _ptr(dh, torch.bfloat16, rows * F, "dh"),
-          _ptr(saved, torch.uint8, rows * 2 * F, "saved"),
-          _ptr(saved_scales, torch.uint8, rows * (2 * F // 32), "saved_scales"),
-          _ptr(row_weights, torch.float32, rows, "row_weights", optional=True), F,
-          _ptr(d_gate_up, torch.bfloat16, rows * 2 * F, "d_gate_up"),
-          _ptr(d_row_weights, torch.float32, rows, "d_row_weights", optional=True), stream=stream)
+          _addr(dh, torch.bfloat16, rows * F, "dh", dev),
+          _addr(saved, torch.uint8, rows * 2 * F, "saved", dev),
+          _addr(saved_scales, torch.uint8, rows * (2 * F // 32), "saved_scales", dev),
+          _opt(row_weights, torch.float32, rows, "row_weights", dev), F,
+          _addr(d_gate_up, torch.bfloat16, rows * 2 * F, "d_gate_up", dev),
+          _opt(d_row_weights, torch.float32, rows, "d_row_weights", dev), stream=stream)
 
 
 # ---------------------------------------------------------------------------

@@ -14,10 +14,12 @@
 // renormalised weights scale / N * (dw_k - sum_j dw_j s_j / N), N = sum_k s.
 //
 // One wave per token, lane l holds experts l, l + 64, ...: the logits are
-// read once, coalesced, and everything else stays in registers.  Sums over
-// tokens are kept per wave in registers, then per workgroup in LDS, then per
-// workgroup in the workspace, and added in a fixed order at each step, so
-// results repeat bit for bit.
+// read once, coalesced, and everything else stays in registers.  The K-th
+// largest of the lanes' maxima bounds the K-th largest key from below; bisection
+// of its bits with a ballot a round finds it.  The keys that reach it, K and a
+// few more, are packed into lanes and ranked by comparing all pairs.  Sums over tokens are kept per wave in
+// registers, then per workgroup in LDS, then per workgroup in the workspace,
+// and added in a fixed order at each step, so results repeat bit for bit.
 #include <algorithm>
 
 #include "moon_rows.h"
@@ -62,7 +64,7 @@ struct RouteGradArgs {
 // below every number, 0 left over for "no candidate".
 __device__ __forceinline__ uint32_t order_key(float x) {
   const uint32_t b = __float_as_uint(x + 0.0f);
-  const uint32_t k = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  const uint32_t k = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
   return x != x ? 1u : k;
 }
 
@@ -70,36 +72,63 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
 }
 
+// Scores up to a common factor: a score is off by |x - shift| 2^-23 and the
+// units of v_exp_f32 and v_rcp_f32.  (The shift is taken off first: its product
+// with log2(e) would overflow, or drown the difference, for large logits.)
+constexpr float kLog2e = 1.44269504088896341f;
+__device__ __forceinline__ float exp_shifted(float x, float shift) {
+  return __builtin_amdgcn_exp2f((x - shift) * kLog2e);
+}
+__device__ __forceinline__ float logistic(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -kLog2e));
+}
+
+// Keys of a wave that are at least t.
+template <int J>
+__device__ __forceinline__ int count_at_least(const uint32_t (&key)[J], uint32_t t) {
+  int n = 0;
+#pragma unroll
+  for (int j = 0; j < J; ++j) n += __popcll(__ballot(key[j] >= t));
+  return n;
+}
+
+__device__ __forceinline__ int lanes_before(uint64_t ballot) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(ballot >> 32),
+                                   __builtin_amdgcn_mbcnt_lo((uint32_t)ballot, 0));
+}
+
+// A key and its expert as one number: larger keys first, then lower ids.
+__device__ __forceinline__ uint64_t pick_of(uint32_t key, int id) {
+  return (uint64_t)key << 32 | (uint32_t)~id;
+}
+__device__ __forceinline__ uint32_t pick_key(uint64_t p) { return (uint32_t)(p >> 32); }
+__device__ __forceinline__ int pick_id(uint64_t p) { return (int)~(uint32_t)p; }
+
 template <bool BF16>
 __device__ __forceinline__ float load_logit(const void* base, int64_t i) {
   if (BF16) return __uint_as_float((uint32_t) static_cast<const uint16_t*>(base)[i] << 16);
   return static_cast<const float*>(base)[i];
 }
 
-// Takes the largest key (two words when Wide) out of the wave; returns its
-// expert, or -1 when no candidate is left.  Among equal keys the lowest id
-// wins: word j holds ids j*64 .. j*64 + 63 by lane.
-template <int J, bool Wide>
-__device__ __forceinline__ int take_largest(uint32_t (&hi)[J], const uint32_t (&lo)[J], int lane,
-                                            uint32_t* key_out) {
+// Takes the largest two-word key out of the wave; returns its expert, or -1
+// when no candidate is left.  Among equal keys the lowest id wins: word j holds
+// ids j*64 .. j*64 + 63 by lane.
+template <int J>
+__device__ __forceinline__ int take_largest(uint32_t (&hi)[J], const uint32_t (&lo)[J], int lane) {
   uint32_t m = hi[0];
 #pragma unroll
   for (int j = 1; j < J; ++j) m = max(m, hi[j]);
   const uint32_t top = wave_max_u32(m);
-  *key_out = top;
   if (top == 0) return -1;
-  uint32_t low = 0;
-  if (Wide) {
-    uint32_t l = 0;
+  uint32_t l = 0;
 #pragma unroll
-    for (int j = 0; j < J; ++j) l = max(l, hi[j] == top ? lo[j] : 0u);
-    low = wave_max_u32(l);
-  }
+  for (int j = 0; j < J; ++j) l = max(l, hi[j] == top ? lo[j] : 0u);
+  const uint32_t low = wave_max_u32(l);
   int id = -1;
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     if (id < 0) {
-      const uint64_t b = __ballot(hi[j] == top && (!Wide || lo[j] == low));
+      const uint64_t b = __ballot(hi[j] == top && lo[j] == low);
       if (b != 0) {
         const int win = __builtin_ctzll(b);
         id = j * kLanes + win;
@@ -131,8 +160,7 @@ __device__ __attribute__((noinline)) int select_wide(const void* logits, int64_t
   }
   int mine = 0;
   for (int k = 0; k < K; ++k) {
-    uint32_t top;
-    const int id = take_largest<J, true>(hi, lo, lane, &top);
+    const int id = take_largest(hi, lo, lane);
     if (lane == k) mine = id;
   }
   return mine;
@@ -173,12 +201,15 @@ __device__ __forceinline__ void finish_rank(const RouteArgs& a, int r, int n, fl
 
 template <int J, bool BF16>
 __global__ void __launch_bounds__(kMaxWaves* kLanes) k_route(RouteArgs a) {
-  extern __shared__ float lds[];  // with stats: [waves][E] sums, [E] counts, [waves] tokens, [waves]
-  const int lane = threadIdx.x & (kLanes - 1), w = threadIdx.x / kLanes;
+  extern __shared__ float lds[];  // [waves][64] picks; with stats also [waves][E] sums,
+                                  // [E] counts, [waves] tokens, [waves]
+  const int lane = threadIdx.x & (kLanes - 1);
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
   const int waves = blockDim.x / kLanes;
   const int r = blockIdx.y, blk = blockIdx.x;
-  float* const red_p = lds;
-  int32_t* const red_c = reinterpret_cast<int32_t*>(lds + waves * a.E);
+  uint64_t* const picks = reinterpret_cast<uint64_t*>(lds) + w * kLanes;
+  float* const red_p = lds + 2 * waves * kLanes;
+  int32_t* const red_c = reinterpret_cast<int32_t*>(red_p + waves * a.E);
   int32_t* const red_n = red_c + a.E;
   float* const red_l = reinterpret_cast<float*>(red_n + waves);
   if (a.stats) {
@@ -194,10 +225,32 @@ __global__ void __launch_bounds__(kMaxWaves* kLanes) k_route(RouteArgs a) {
     bias[j] = biased && e < a.E ? a.bias[e] : 0.0f;
   }
   int32_t n_valid = 0;
-  for (int t = blk * waves + w; t < a.S; t += a.nblk * waves) {
+  // The next token's logits are on their way while one is worked on.
+  const int step = a.nblk * waves;
+  float ahead[J];
+  uint32_t ahead_ok = 1;
+  const auto fetch = [&](int t) {
+    const int64_t tok = (int64_t)r * a.S + t;
+    if (a.valid != nullptr) ahead_ok = a.valid[tok];
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      ahead[j] = load_logit<BF16>(a.logits, tok * a.E + min(j * kLanes + lane, a.E - 1));
+  };
+  if (blk * waves + w < a.S) fetch(blk * waves + w);
+  for (int t = blk * waves + w; t < a.S; t += step) {
     const int64_t tok = (int64_t)r * a.S + t;
     const int64_t at = tok * a.E;
-    if (a.valid != nullptr && a.valid[tok] == 0) {  // one token, so the whole wave agrees
+    const int ok = __builtin_amdgcn_readfirstlane((int)ahead_ok);
+    float s[J];
+    uint32_t key[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      s[j] = ahead[j];
+      const uint32_t k = order_key(s[j]);
+      key[j] = j * kLanes + lane < a.E ? k : 0u;
+    }
+    if (t + step < a.S) fetch(t + step);
+    if (ok == 0) {
       if (lane < a.K) {
         a.topk[tok * a.K + lane] = 0;
         a.weights[tok * a.K + lane] = 0.0f;
@@ -205,32 +258,27 @@ __global__ void __launch_bounds__(kMaxWaves* kLanes) k_route(RouteArgs a) {
       continue;
     }
     ++n_valid;
-    float s[J];
-    uint32_t key[J];
-    float shift = 0.0f;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int e = j * kLanes + lane;
-      s[j] = e < a.E ? load_logit<BF16>(a.logits, at + e) : 0.0f;
-      key[j] = e < a.E ? order_key(s[j]) : 0u;
-    }
-    if (a.sigmoid) {
+    if (a.sigmoid && (biased || a.stats)) {
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         const float x = s[j];
-        s[j] = sigmoid_f32(x);
+        s[j] = logistic(x);
         if (biased && key[j] != 0u && x != -INFINITY) key[j] = order_key(s[j] + bias[j]);
       }
-    } else {
-      uint32_t m = key[0];
+    }
+    uint32_t mine = key[0];
 #pragma unroll
-      for (int j = 1; j < J; ++j) m = max(m, key[j]);
-      m = wave_max_u32(m);
+    for (int j = 1; j < J; ++j) mine = max(mine, key[j]);
+    const uint32_t top = wave_max_u32(mine);
+    float shift = 0.0f;
+    if (!a.sigmoid) {
       // Nothing but masked experts or NaN: scores 0 (NaN) with no shift.
-      const float top = key_value(m);
-      shift = m == 1u || top == -INFINITY ? 0.0f : top;
+      const float m = key_value(top);
+      shift = top == 1u || m == -INFINITY ? 0.0f : m;
+      if (a.stats || !a.renorm) {
 #pragma unroll
-      for (int j = 0; j < J; ++j) s[j] = exp_f32(s[j] - shift);
+        for (int j = 0; j < J; ++j) s[j] = exp_shifted(s[j], shift);
+      }
     }
     float total = 0.0f;
     if (a.stats || !a.renorm) {
@@ -241,51 +289,106 @@ __global__ void __launch_bounds__(kMaxWaves* kLanes) k_route(RouteArgs a) {
       }
       total = wave_sum(total);
     }
-    int mine = 0;
-    uint32_t my_key = 0;
-    float prev = 0.0f;
-    bool close = false;
-    for (int k = 0; k < a.K; ++k) {
-      uint32_t top;
-      const int id = take_largest<J, false>(key, key, lane, &top);
-      if (lane == k) {
-        mine = id;
-        my_key = top;
+    // At least K of the lanes' maxima are >= lo (min(E, 64) lanes have one),
+    // fewer than K are >= hi.
+    uint32_t lo = wave_min_u32(mine == 0u ? ~0u : mine), hi = top + 1u;
+    // A few maxima too many cost less than the rounds that would tell them,
+    // unless every pair is looked at twice.
+    const int enough = biased ? a.K : a.K + (a.K >> 1);
+    while (hi - lo > 1u) {
+      const uint32_t mid = lo + (hi - lo) / 2;
+      const int n = __popcll(__ballot(mine >= mid));
+      if (n < a.K) {
+        hi = mid;
+      } else {
+        lo = mid;
+        if (n <= enough) break;
       }
-      const float v = key_value(top);
-      close = close || (k > 0 && prev - v <= 1e-6f * fmaxf(1.0f, fabsf(v)));
-      prev = v;
     }
+    int found = count_at_least(key, lo);
+    const bool crowded = found > kLanes;
+    int at_pick = 0;
+    if (!crowded) {
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const uint64_t b = __ballot(key[j] >= lo);
+        if (key[j] >= lo) picks[at_pick + lanes_before(b)] = pick_of(key[j], j * kLanes + lane);
+        at_pick += __popcll(b);
+      }
+    } else {
+      // Too many for the lanes (long runs of equal keys): on by all keys, and of
+      // those equal at the end the first ones, as many as there is room for.
+      hi = top + 1u;
+      while (hi - lo > 1u) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        if (count_at_least(key, mid) >= a.K)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      found = a.K;
+      const int room = a.K - count_at_least(key, lo + 1u);
+      int ties = 0;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const uint64_t eq = __ballot(key[j] == lo);
+        const bool in = key[j] > lo || (key[j] == lo && ties + lanes_before(eq) < room);
+        const uint64_t b = __ballot(in);
+        if (in) picks[at_pick + lanes_before(b)] = pick_of(key[j], j * kLanes + lane);
+        at_pick += __popcll(b);
+        ties += __popcll(eq);
+      }
+    }
+    wave_lds_sync();
+    const uint64_t p = picks[min(lane, found - 1)];
+    int rank = lane < found ? 0 : kLanes;
+    const float v = key_value(pick_key(p));
+#pragma unroll 4
+    for (int k = 0; k < found; ++k) rank += picks[k] > p ? 1 : 0;
+    bool close = false;  // another pick is hard to tell from this one, which counts
+    if (biased) {
+      const float near = 1e-6f * fmaxf(1.0f, fabsf(v));
+      int n = 0;
+#pragma unroll 4
+      for (int k = 0; k < found; ++k)
+        n += fabsf(key_value(pick_key(picks[k])) - v) <= near ? 1 : 0;
+      close = n > 1 && rank < a.K;  // itself is one
+    }
+    wave_lds_sync();
+    int id = pick_id(p);
     float sel;
     if (biased) {
-      uint32_t next = key[0];
+      uint32_t next = 0;  // the largest key that is not among the picks
 #pragma unroll
-      for (int j = 1; j < J; ++j) next = max(next, key[j]);
-      const float v = key_value(wave_max_u32(next));
-      close = close || prev - v <= 1e-6f * fmaxf(1.0f, fabsf(v));
+      for (int j = 0; j < J; ++j) next = max(next, key[j] < lo ? key[j] : 0u);
+      const float border = key_value(lo), left = key_value(wave_max_u32(next));
+      close = close || crowded || border - left <= 1e-6f * fmaxf(1.0f, fabsf(border));
       // A score in 32 bits plus its bias is off by a few units in the last
       // place, below 5e-7 * max(1, |sum|): neighbours nearer than twice that
       // are told apart in 64 bits.
-      if (close) mine = select_wide<J, BF16>(a.logits, at, a.bias, a.E, a.K, lane);
-      sel = lane < a.K ? sigmoid_f32(load_logit<BF16>(a.logits, at + mine)) : 0.0f;
+      if (__ballot(close) != 0) {
+        id = select_wide<J, BF16>(a.logits, at, a.bias, a.E, a.K, lane);
+        rank = lane;
+      }
+      sel = rank < a.K ? logistic(load_logit<BF16>(a.logits, at + id)) : 0.0f;
     } else {
-      const float x = my_key == 1u ? NAN : key_value(my_key);
-      sel = lane < a.K ? (a.sigmoid ? sigmoid_f32(x) : exp_f32(x - shift)) : 0.0f;
+      const float x = pick_key(p) == 1u ? NAN : v;
+      sel = rank < a.K ? (a.sigmoid ? logistic(x) : exp_shifted(x, shift)) : 0.0f;
     }
     float out;
     if (a.renorm)
       out = a.scale * (sel * reciprocal_or_zero(wave_sum(sel)));
     else
       out = a.scale * (a.sigmoid ? sel : sel * reciprocal_or_zero(total));
-    if (lane < a.K) {
-      a.topk[tok * a.K + lane] = mine;
-      a.weights[tok * a.K + lane] = out;
+    if (rank < a.K) {
+      a.topk[tok * a.K + rank] = id;
+      a.weights[tok * a.K + rank] = out;
     }
     if (a.stats) {
       const float inv = reciprocal_or_zero(total);
 #pragma unroll
-      for (int j = 0; j < J; ++j) acc[j] += s[j] * inv;
-      if (lane < a.K) atomicAdd(&red_c[mine], 1);  // whole numbers: any order
+      for (int j = 0; j < J; ++j) acc[j] = fmaf(s[j], inv, acc[j]);
+      if (rank < a.K) atomicAdd(&red_c[id], 1);  // whole numbers: any order
     }
   }
   if (!a.stats) return;
@@ -314,29 +417,48 @@ __global__ void __launch_bounds__(kMaxWaves* kLanes) k_route(RouteArgs a) {
   if (threadIdx.x == 0) a.part_n[row] = n;
 }
 
-__global__ void __launch_bounds__(kMaxExperts) k_route_finish(RouteArgs a) {
-  __shared__ float red[kMaxExperts / kLanes];
+// Adds the workgroups' sums of a rank: 1024 threads, as many to an expert as
+// there are, each a fixed share of the partial sums.
+__global__ void __launch_bounds__(1024) k_route_finish(RouteArgs a, int experts) {
+  __shared__ float red[1024 / kLanes];
+  __shared__ float part_p[1024];
+  __shared__ int32_t part_c[1024];
+  __shared__ int32_t tokens;
   const int r = blockIdx.x;
   const int64_t row = (int64_t)r * a.nblk;
+  const int e = threadIdx.x % experts, share = threadIdx.x / experts, shares = 1024 / experts;
+  if (threadIdx.x == 0) tokens = 0;
+  __syncthreads();
   int32_t n = 0;
-  for (int i = 0; i < a.nblk; ++i) n += a.part_n[row + i];
-  finish_rank(a, r, n, red, [&](int e, float* p, int32_t* c) {
-    float sum = 0.0f;
-    int32_t cnt = 0;
-#pragma unroll 8
-    for (int i = 0; i < a.nblk; ++i) {
+  for (int i = threadIdx.x; i < a.nblk; i += 1024) n += a.part_n[row + i];
+  if (n != 0) atomicAdd(&tokens, n);  // whole numbers: any order
+  float sum = 0.0f;
+  int32_t cnt = 0;
+  if (e < a.E) {
+#pragma unroll 4
+    for (int i = share; i < a.nblk; i += shares) {
       sum += a.part_p[(row + i) * a.E + e];
       cnt += a.part_c[(row + i) * a.E + e];
     }
-    *p = sum;
-    *c = cnt;
+  }
+  part_p[threadIdx.x] = sum;
+  part_c[threadIdx.x] = cnt;
+  __syncthreads();
+  finish_rank(a, r, tokens, red, [&](int x, float* p, int32_t* c) {
+    *p = 0.0f;
+    *c = 0;
+    for (int i = 0; i < shares; ++i) {
+      *p += part_p[i * experts + x];
+      *c += part_c[i * experts + x];
+    }
   });
 }
 
 template <int J, bool BF16>
 __global__ void __launch_bounds__(256) k_route_grad(RouteGradArgs a, int nblk) {
   __shared__ float lds[4][J * kLanes];
-  const int lane = threadIdx.x & (kLanes - 1), w = threadIdx.x / kLanes;
+  const int lane = threadIdx.x & (kLanes - 1);
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
   const int r = blockIdx.y;
   float b[J];
   {
@@ -379,7 +501,7 @@ __global__ void __launch_bounds__(256) k_route_grad(RouteGradArgs a, int nblk) {
       float total = 0.0f;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        s[j] = a.sigmoid ? sigmoid_f32(x[j]) : exp_f32(x[j] - shift);
+        s[j] = a.sigmoid ? logistic(x[j]) : exp_shifted(x[j], shift);
         total += s[j];
       }
       total = wave_sum(total);
@@ -391,7 +513,7 @@ __global__ void __launch_bounds__(256) k_route_grad(RouteGradArgs a, int nblk) {
         float sel = 0.0f;
         if (ok) {
           const float v = load_logit<BF16>(a.logits, at + id);
-          sel = a.sigmoid ? sigmoid_f32(v) : exp_f32(v - shift);
+          sel = a.sigmoid ? logistic(v) : exp_shifted(v, shift);
         }
         float g;
         if (a.renorm) {
@@ -419,7 +541,7 @@ __global__ void __launch_bounds__(256) k_route_grad(RouteGradArgs a, int nblk) {
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         if (a.sigmoid)
-          d[j] = s[j] * sigmoid_f32(-x[j]) * (d[j] + (b[j] - dot) * inv);
+          d[j] = s[j] * logistic(-x[j]) * (d[j] + (b[j] - dot) * inv);
         else
           d[j] = s[j] * (d[j] + (b[j] - dot) * inv);
       }
@@ -439,7 +561,7 @@ __global__ void __launch_bounds__(256) k_route_grad(RouteGradArgs a, int nblk) {
 
 // How a call is cut: waves per workgroup and workgroups per rank.  Up to 256
 // tokens a rank one workgroup of 16 waves does it all in one launch; beyond
-// that workgroups of four waves, enough to fill the GPU (2048 in all), and a
+// that workgroups of eight waves, three to a compute unit (768 in all), and a
 // second launch adds their partial sums.  Without counts, sums or loss there
 // is nothing to add and every four tokens get a workgroup.
 void route_cut(int R, int S, bool stats, int* waves, int* nblk) {
@@ -448,9 +570,9 @@ void route_cut(int R, int S, bool stats, int* waves, int* nblk) {
     *nblk = 1;
     return;
   }
-  *waves = 4;
-  const int want = (S + 3) / 4;
-  *nblk = stats ? std::max(1, std::min(want, 2048 / R)) : std::min(want, 65536);
+  *waves = stats ? 8 : 4;
+  const int want = (S + *waves - 1) / *waves;
+  *nblk = std::min(want, stats ? std::max(2, 768 / R) : 65536);
 }
 
 size_t route_workspace(int R, int S, int E, bool stats) {
@@ -461,11 +583,13 @@ size_t route_workspace(int R, int S, int E, bool stats) {
 
 template <int J, bool BF16>
 hipError_t run_route(const RouteArgs& a, int waves, hipStream_t s) {
-  const size_t lds = a.stats ? ((size_t)waves * a.E + a.E + 2 * waves) * 4 : 0;
+  const size_t lds = ((size_t)waves * kLanes * 2 + (a.stats ? (size_t)waves * a.E + a.E + 2 * waves : 0)) * 4;
   hipLaunchKernelGGL((k_route<J, BF16>), dim3(a.nblk, a.R), dim3(waves * kLanes), lds, s, a);
-  if (a.stats && a.nblk > 1)
-    hipLaunchKernelGGL(k_route_finish, dim3(a.R), dim3((a.E + kLanes - 1) / kLanes * kLanes), 0, s,
-                       a);
+  if (a.stats && a.nblk > 1) {
+    int experts = kLanes;  // the power of two that holds E
+    while (experts < a.E) experts *= 2;
+    hipLaunchKernelGGL(k_route_finish, dim3(a.R), dim3(1024), 0, s, a, experts);
+  }
   return hipGetLastError();
 }
 

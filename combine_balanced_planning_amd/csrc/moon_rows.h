@@ -111,6 +111,9 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
+// Smallest value of the wave.
+__device__ __forceinline__ uint32_t wave_min_u32(uint32_t v) { return ~wave_max_u32(~v); }
+
 template <int Ctrl, int Rows>
 __device__ __forceinline__ float dpp_add(float v) {
   return v + __uint_as_float(dpp_u32<Ctrl, Rows>(0u, __float_as_uint(v)));

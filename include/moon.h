@@ -319,7 +319,8 @@ moon_status moon_route_workspace(const moon_route_config* cfg, size_t* bytes);
  * and makes NaN what its score enters (weights renormalised over picked
  * experts only where it is picked).
  * valid_rs [R,S] (optional): a 0 marks a token outside the batch, whose logits
- * are not read, whose ids and weights are 0 and which the balance leaves out.
+ * have no effect (NaN neither), whose ids and weights are 0 and which the balance
+ * leaves out.
  * Optional outputs, NULL where not wanted:
  *   tokens_per_expert_re [R,E]  histogram of the ids written (the marked
  *                               tokens' zeros included): moon_plan's input
