@@ -73,101 +73,6 @@ __device__ __forceinline__ void zero_rows(uint16_t* y, int64_t row0, int rows, i
     *reinterpret_cast<vec4u*>(y + (row0 + i / vecs) * N + n0 + i % vecs * 8) = zero;
 }
 
-// Few rows per group: the weights are read once and bound the time.  A
-// workgroup takes 32 outputs of one group; its four waves split K, each
-// streaming 512 values at a time straight into the matrix cores, and add up
-// in LDS.
-template <int MT, bool Swiglu>
-__global__ void __launch_bounds__(256) k_expert_stream(ExpertArgs a, Groups g) {
-  constexpr int P = Swiglu ? 2 : 1, NT = 2;
-  __shared__ vec4f red[4][P][NT][MT][kLanes];
-  if (g.status[0] != 0) return;
-  const int u = blockIdx.y / g.per, j = blockIdx.y % g.per;
-  const Span sp = group_span(g, u, j);
-  const int n0 = blockIdx.x * 16 * NT;
-  const int64_t base = (int64_t)u * g.NvS;
-  zero_rows(a.y, base + sp.real_end, sp.end - sp.real_end, a.N, n0, 16 * NT);
-  const int lane = threadIdx.x & (kLanes - 1), w = threadIdx.x / kLanes;
-  const int r16 = lane & 15, kb = lane >> 4;
-  const int blocks = a.K / 32;
-  const uint8_t *wq[P], *ws[P];
-#pragma unroll
-  for (int p = 0; p < P; ++p) weight_of(g, a.w[p], u, j, a.N, a.K, &wq[p], &ws[p]);
-  for (int m0 = sp.begin; m0 < sp.real_end; m0 += 16 * MT) {
-    const int left = sp.real_end - m0;
-    vec4f acc[P][NT][MT];
-#pragma unroll
-    for (int p = 0; p < P; ++p)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) acc[p][n][m] = vec4f{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int c = w * 16; c < blocks; c += 64) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int b = c + 4 * i + kb;
-        const bool in = b < blocks;
-        const int bb = in ? b : 0;
-        vec4u xv[MT];
-        uint32_t xsc[MT];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const int64_t row = base + min(m0 + 16 * m + r16, sp.real_end - 1);
-          xv[m] = *reinterpret_cast<const vec4u*>(a.xq + (row * blocks + bb) * 16);
-          xsc[m] = a.xs[row * blocks + bb];
-          if (!in) {
-            xv[m] = vec4u{0u, 0u, 0u, 0u};
-            xsc[m] = 127u;
-          }
-        }
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const int64_t row = min(n0 + 16 * n + r16, a.N - 1);
-            vec4u wv = *reinterpret_cast<const vec4u*>(wq[p] + (row * blocks + bb) * 16);
-            uint32_t wsc = ws[p][row * blocks + bb];
-            if (!in) {
-              wv = vec4u{0u, 0u, 0u, 0u};
-              wsc = 127u;
-            }
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-              if (16 * m < left) acc[p][n][m] = mfma4(wv, xv[m], acc[p][n][m], wsc, xsc[m]);
-          }
-      }
-    }
-    __syncthreads();  // the last tile's sums are read
-#pragma unroll
-    for (int p = 0; p < P; ++p)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) red[w][p][n][m][lane] = acc[p][n][m];
-    __syncthreads();
-    for (int t = w; t < NT * MT; t += 4) {
-      const int n = t % NT, m = t / NT;
-      const int row = m0 + 16 * m + r16, col = n0 + 16 * n + 4 * kb;
-      if (row >= sp.real_end || col >= a.N) continue;
-      vec4f s[P];
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-        s[p] = (red[0][p][n][m][lane] + red[1][p][n][m][lane]) +
-               (red[2][p][n][m][lane] + red[3][p][n][m][lane]);
-      vec4f o = s[0];
-      if (Swiglu) o = gated(s[0], s[P - 1], a.row_w != nullptr ? a.row_w[base + row] : 1.0f);
-      *reinterpret_cast<vec2u*>(a.y + (base + row) * a.N + col) = round4(o);
-    }
-  }
-}
-
-// ---- many rows per group: tiles of 256 weight rows by 256 window rows ----
-
-constexpr int kTileWaves = 8;
-constexpr int kTileThreads = kTileWaves * kLanes;
-constexpr int kTile = 256;
-constexpr int kMaxEntries = 1024;  // of the tile table
-
 // `bytes` bytes from p as a buffer: loads beyond them read nothing and give 0.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint8_t* p, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, (int)bytes, 0x00027000);
@@ -187,6 +92,204 @@ __device__ __forceinline__ void wait_vm() {
 __device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(0xC07F); }
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// ---- few rows per group: the weights are read once and bound the time ----
+
+// A workgroup takes 64 weight rows of one group (with a gate 32 of each
+// matrix) and its window rows, 16 * MT at a time.  K advances by 256 values, 128
+// bytes of a row, a step; LDS holds four steps, loaded straight into it eight
+// lanes a row, three steps ahead.  The 16-byte blocks of a row are stored
+// swapped by its index, so ds_read_b128 of 16 rows meets no bank twice.  Each of
+// the four waves owns 16 outputs; with a gate two, and the waves of a pair take
+// turns along K and add up at the end.
+template <int MT, bool Swiglu, bool Whole>
+__global__ void __launch_bounds__(256) k_expert_stream(ExpertArgs a, Groups g) {
+  constexpr int P = Swiglu ? 2 : 1;
+  constexpr int kOut = 64 / P, kRows = 64 + 16 * MT, kXLoads = MT < 2 ? 1 : MT / 2;
+  constexpr int kLoads = 2 + kXLoads;  // of a wave, a step
+  __shared__ vec4u st0[kRows * 8], st1[kRows * 8], st2[kRows * 8], st3[kRows * 8];
+  __shared__ vec4u sc[2][kRows];
+  if (g.status[0] != 0) return;
+  const int u = blockIdx.y / g.per, j = blockIdx.y % g.per;
+  const Span sp = group_span(g, u, j);
+  const int n0 = blockIdx.x * kOut;
+  const int64_t base = (int64_t)u * g.NvS;
+  zero_rows(a.y, base + sp.real_end, sp.end - sp.real_end, a.N, n0, kOut);
+  const int tid = threadIdx.x, lane = tid & (kLanes - 1);
+  const int w = __builtin_amdgcn_readfirstlane(tid / kLanes);
+  const int r16 = lane & 15, kb = lane >> 4;
+  const int blocks = a.K / 32, steps = (blocks + 7) / 8;
+  const uint32_t row_bytes = 16u * blocks;
+  const int nr = min(kOut, a.N - n0);  // weight rows of each matrix
+  const uint8_t *wq[2], *ws[2];
+  weight_of(g, a.w[0], u, j, a.N, a.K, &wq[0], &ws[0]);
+  weight_of(g, a.w[P - 1], u, j, a.N, a.K, &wq[1], &ws[1]);
+  const __amdgpu_buffer_rsrc_t wsrc =
+      buffer(wq[Swiglu ? w >> 1 : 0] + (int64_t)n0 * row_bytes, nr * row_bytes);
+  // A load takes eight rows; the block that this lane takes of its row, for the
+  // first and the second half of 16 rows.
+  const uint32_t blk16[2] = {16u * ((lane & 7) ^ (lane >> 4)), 16u * ((lane & 7) ^ (4 + (lane >> 4)))};
+  const uint32_t wat = ((Swiglu ? w & 1 : w) * 16 + (lane >> 3)) * row_bytes;
+  for (int m0 = sp.begin; m0 < sp.real_end; m0 += 16 * MT) {
+    const int left = min(sp.real_end - m0, 16 * MT);
+    const __amdgpu_buffer_rsrc_t xsrc = buffer(a.xq + (base + m0) * row_bytes, left * row_bytes);
+    // Blocks behind a row's end are the next row's (or zeros): their scales, of
+    // both operands, are 2^-127, and what they add vanishes in fp32.
+    const auto fill = [&](vec4u* st, int step) {
+      const uint32_t at = step < steps ? step * 128u : 0x80000000u;  // nothing behind the last
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        load_lds16(wsrc, wat + i * 8 * row_bytes + blk16[i] + at, st + (w * 2 + i) * kLanes);
+#pragma unroll
+      for (int i = 0; i < kXLoads; ++i) {
+        const int blk = (MT < 2 ? w & 1 : w * kXLoads + i);  // eight rows
+        load_lds16(xsrc, (blk * 8 + (lane >> 3)) * row_bytes + blk16[MT < 2 ? w & 1 : i & 1] + at,
+                   st + 64 * 8 + blk * kLanes);
+      }
+    };
+    // Scales of 512 values of this thread's row (weights, then window rows);
+    // unless K is Whole turns of them, byte by byte at the row's end.
+    const uint8_t* const wscale = tid < kOut ? ws[0] : ws[1];
+    const uint8_t* const scale_row =
+        tid < 64 ? wscale + (int64_t)(n0 + min(tid % kOut, nr - 1)) * blocks
+                 : a.xs + (base + m0 + min(tid - 64, left - 1)) * blocks;
+    const auto get_scales = [&](int turn) {
+      vec4u v = {0u, 0u, 0u, 0u};
+      if (Whole) {
+        __builtin_memcpy(&v, scale_row + min(turn * 16, blocks - 16), 16);
+        if (turn * 16 >= blocks) v = vec4u{0u, 0u, 0u, 0u};
+        return v;
+      }
+      if (tid >= kRows) return v;
+      if (turn * 16 + 16 <= blocks) {
+        __builtin_memcpy(&v, scale_row + turn * 16, 16);
+      } else {
+#pragma unroll 1
+        for (int k = 0; k < 16; ++k) {  // bytes move in from the top
+          const int n = turn * 16 + k;
+          const uint32_t in = n < blocks ? scale_row[n] : 0u;
+          v.x = v.x >> 8 | v.y << 24;
+          v.y = v.y >> 8 | v.z << 24;
+          v.z = v.z >> 8 | v.w << 24;
+          v.w = v.w >> 8 | in << 24;
+        }
+      }
+      return v;
+    };
+    vec4f acc[P][MT];
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) acc[p][m] = vec4f{0.0f, 0.0f, 0.0f, 0.0f};
+    vec4u even = get_scales(0), odd = get_scales(1);
+    fill(st0, 0);
+    fill(st1, 1);
+    fill(st2, 2);
+    if (tid < kRows) sc[0][tid] = even;
+    const int in_frag = (r16 >> 3) * 64 + (r16 & 7) * 8;
+    const int shift = 8 * kb;
+    // Values 128 * sub .. of a step: products of the wave's fragments; d picks
+    // the scales' word of the turn's four.
+    const auto products = [&](const vec4u* st, const vec4u (&sv)[P], const vec4u (&sx)[MT], int sub,
+                              int d) {
+      const int c = (4 * sub + kb) ^ (r16 >> 1);
+      vec4u wv[P], xv[MT];
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+        wv[p] = st[(Swiglu ? p * 2 + (w & 1) : w) * 128 + in_frag + c];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) xv[m] = st[512 + m * 128 + in_frag + c];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+        if (16 * m < left)
+#pragma unroll
+          for (int p = 0; p < P; ++p)
+            acc[p][m] = mfma4(wv[p], xv[m], acc[p][m], sv[p][d] >> shift, sx[m][d] >> shift);
+    };
+    const auto both = [&](const vec4u* st, const vec4u (&sv)[P], const vec4u (&sx)[MT], int half) {
+      if (Swiglu) {
+        const int sub = w >> 1;
+        if (sub == 0)
+          products(st, sv, sx, 0, 2 * half);
+        else
+          products(st, sv, sx, 1, 2 * half + 1);
+      } else {
+        products(st, sv, sx, 0, 2 * half);
+        products(st, sv, sx, 1, 2 * half + 1);
+      }
+    };
+    vec4u sv[P], sx[MT];
+    const auto read_scales = [&](int buf) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) sv[p] = sc[buf][(Swiglu ? p * 32 + (w & 1) * 16 : w * 16) + r16];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) sx[m] = sc[buf][64 + m * 16 + r16];
+    };
+    // Four steps, two turns of scales, a round; the buffer before THIS has been
+    // read by every wave once the barrier is passed and takes the step after
+    // the two on their way.
+#define MOON_STEP(S, THIS, FREE)                       \
+  {                                                    \
+    wait_vm<2 * kLoads>();                             \
+    wait_lds();                                        \
+    asm volatile("" ::: "memory");                     \
+    __builtin_amdgcn_s_barrier();                      \
+    asm volatile("" ::: "memory");                     \
+    fill(FREE, s + S + 3);                             \
+    if (S == 0 || S == 2) read_scales(S / 2);          \
+    both(THIS, sv, sx, S & 1);                         \
+  }
+#pragma unroll 1
+    for (int s = 0; s < steps; s += 4) {
+      even = get_scales(s / 2 + 2);  // on their way for three steps
+      MOON_STEP(0, st0, st3)
+      MOON_STEP(1, st1, st0)
+      if (tid < kRows) sc[1][tid] = odd;
+      odd = get_scales(s / 2 + 3);
+      MOON_STEP(2, st2, st1)
+      MOON_STEP(3, st3, st2)
+      if (tid < kRows) sc[0][tid] = even;
+    }
+#undef MOON_STEP
+    wait_vm<0>();
+    __syncthreads();
+    if (Swiglu) {
+      vec4f* const red = reinterpret_cast<vec4f*>(st0);
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          if (w >= 2) red[(((w & 1) * P + p) * MT + m) * kLanes + lane] = acc[p][m];
+      __syncthreads();
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          if (w < 2) acc[p][m] += red[((w * P + p) * MT + m) * kLanes + lane];
+    }
+    if (!Swiglu || w < 2) {
+      const int col = n0 + w * 16 + 4 * kb;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const int row = 16 * m + r16;
+        if (row < left && col < a.N) {
+          const int64_t at = base + m0 + row;
+          vec4f o = acc[0][m];
+          if (Swiglu) o = gated(o, acc[P - 1][m], a.row_w != nullptr ? a.row_w[at] : 1.0f);
+          *reinterpret_cast<vec2u*>(a.y + at * a.N + col) = round4(o);
+        }
+      }
+    }
+    __syncthreads();  // LDS is free for the next rows
+  }
+}
+
+// ---- many rows per group: tiles of 256 weight rows by 256 window rows ----
+
+constexpr int kTileWaves = 8;
+constexpr int kTileThreads = kTileWaves * kLanes;
+constexpr int kTile = 256;
+constexpr int kMaxEntries = 1024;  // of the tile table
 
 // The thread's index as a value the compiler knows nothing of: what follows
 // from it is worked out where it is used, not kept in registers across the
@@ -621,8 +724,21 @@ moon_status launch(const ExpertArgs& a, const Groups& g, hipStream_t s) {
       hipLaunchKernelGGL((k_expert_tiles<Swiglu, false>), dim3(wgs), dim3(kTileThreads), 0, s, a, g);
     return hipGetLastError() == hipSuccess ? MOON_OK : MOON_ERR_HIP;
   }
-  const dim3 grid((a.N + 31) / 32, g.R * g.per);
-  hipLaunchKernelGGL((k_expert_stream<4, Swiglu>), grid, dim3(256), 0, s, a, g);
+  // Up to eight rows a group on average: 16 at a time hold nearly every group;
+  // beyond that 64, so that a group's weights are read once.
+  const dim3 grid(Swiglu ? (a.N + 31) / 32 : (a.N + 63) / 64, g.R * g.per);
+  const bool few = rows <= 8 * (int64_t)g.E;
+  if (a.K % 512 == 0) {
+    if (few)
+      hipLaunchKernelGGL((k_expert_stream<1, Swiglu, true>), grid, dim3(256), 0, s, a, g);
+    else
+      hipLaunchKernelGGL((k_expert_stream<4, Swiglu, true>), grid, dim3(256), 0, s, a, g);
+  } else {
+    if (few)
+      hipLaunchKernelGGL((k_expert_stream<1, Swiglu, false>), grid, dim3(256), 0, s, a, g);
+    else
+      hipLaunchKernelGGL((k_expert_stream<4, Swiglu, false>), grid, dim3(256), 0, s, a, g);
+  }
   return hipGetLastError() == hipSuccess ? MOON_OK : MOON_ERR_HIP;
 }
 

@@ -133,6 +133,16 @@ def own(R, E, B, rows, slots=None):
     ("long", 1, 1, 1, 1, [3], None, 8192, 16),
     ("more slots than experts", 2, 2, 4, 1, [3, 4], [[2, 0, 0, 0], [0, 0, 0, 0]], 64, 32),
     ("large tiles", 2, 4, 2, 16, [700, 0, 513, 256], [[255, 0], [31, 0]], 1056, 520),
+    ("one large group among small ones", 1, 16, 1, 1, [40] + [1] * 15, None, 512, 72),
+    ("the same, ragged K", 1, 16, 1, 1, [1] * 15 + [33], None, 608, 40),
+    ("whole turns, odd number", 2, 16, 2, 4, [2, 3] * 8, [[1, 0], [5, 0]], 1536, 136),
+    ("middling groups", 2, 4, 1, 8, [40, 70, 64, 17], [[20], [0]], 1024, 264),
+    ("middling, six steps", 2, 4, 1, 8, [40, 70, 64, 17], [[20], [0]], 1536, 64),
+    ("tiles, one turn", 1, 2, 1, 1, [257, 300], None, 512, 264),
+    ("tiles, two turns", 2, 4, 1, 16, [300, 513, 0, 256], [[190], [0]], 1024, 256),
+    ("tiles, three turns", 1, 1, 1, 1, [600], None, 1536, 392),
+    ("tiles, a few columns", 1, 1, 1, 1, [1000], None, 512, 8),
+    ("tiles, the shortest K", 1, 2, 1, 1, [200, 129], None, 32, 48),
 ])
 def test_products(env, label, R, E, B, P, rows, slots, K, N):
     say(f"[case] products {label}: R={R} E={E} B={B} P={P} K={K} N={N}")
