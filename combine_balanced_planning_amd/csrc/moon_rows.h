@@ -136,6 +136,13 @@ __device__ __forceinline__ uint32_t quad_max_u32(uint32_t v) {
   return max(v, dpp_u32<0x4E, 0xF>(0, v));
 }
 
+// One byte of each quad of a 16-lane row as a word, in every lane of the row.
+__device__ __forceinline__ uint32_t quad_bytes(uint32_t b) {
+  uint32_t v = b << (8 * ((threadIdx.x >> 2) & 3));
+  v |= dpp_u32<0x124, 0xF>(0, v);  // row_ror:4
+  return v | dpp_u32<0x128, 0xF>(0, v);  // row_ror:8
+}
+
 // Orders LDS accesses of one wave's lanes among each other (the hardware runs
 // them in order; this keeps the compiler from moving them).
 __device__ __forceinline__ void wave_lds_sync() {

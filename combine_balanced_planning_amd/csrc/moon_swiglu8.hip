@@ -183,7 +183,7 @@ moon_status check(SwigluArgs* a, const moon_plan_arrays* plan, Groups* g) {
   a->lanes = kLanes;
   while (a->lanes > 4 && a->lanes / 2 >= a->F / 8) a->lanes /= 2;
   const int64_t rows = (int64_t)g->R * g->NvS;
-  a->per_wg = (int)std::max<int64_t>(1, std::min<int64_t>(64, rows / 4096));
+  a->per_wg = (int)std::max<int64_t>(1, std::min<int64_t>(64, rows / 16384));
   a->per_wg = std::max(a->per_wg, std::min(64, 256 / a->lanes));
   return MOON_OK;
 }
