@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(1024) k_route_finish(RouteArgs a, int experts)
 
 template <int J, bool BF16>
 __global__ void __launch_bounds__(256) k_route_grad(RouteGradArgs a, int nblk) {
-  __shared__ float lds[4][J * kLanes];
+  __shared__ float lds[4][J * kLanes];  // a wave's experts, by id
   const int lane = threadIdx.x & (kLanes - 1);
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
   const int r = blockIdx.y;
@@ -475,25 +475,46 @@ __global__ void __launch_bounds__(256) k_route_grad(RouteGradArgs a, int nblk) {
                  ? base * (float)(a.counts[r * a.E + e] - (e == 0 ? pads : 0)) : 0.0f;
     }
   }
-  for (int t = blockIdx.x * 4 + w; t < a.S; t += nblk * 4) {
+  // The next token's logits, ids and weight gradients are on their way while
+  // one is worked on.
+  const int step = nblk * 4;
+  float ahead[J], ahead_dw = 0.0f;
+  int32_t ahead_id = -1;
+  uint32_t ahead_ok = 1;
+  const auto fetch = [&](int t) {
     const int64_t tok = (int64_t)r * a.S + t;
-    const int64_t at = tok * a.E;
-    float d[J];
-    if (a.valid != nullptr && a.valid[tok] == 0) {
+    if (a.valid != nullptr) ahead_ok = a.valid[tok];
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      ahead[j] = load_logit<BF16>(a.logits, tok * a.E + min(j * kLanes + lane, a.E - 1));
+    if (a.d_weights != nullptr && lane < a.K) {
+      ahead_id = a.topk[tok * a.K + lane];
+      ahead_dw = a.d_weights[tok * a.K + lane];
+    }
+  };
+  if ((int)blockIdx.x * 4 + w < a.S) fetch(blockIdx.x * 4 + w);
+  for (int t = blockIdx.x * 4 + w; t < a.S; t += step) {
+    const int64_t at = ((int64_t)r * a.S + t) * a.E;
+    const int ok = __builtin_amdgcn_readfirstlane((int)ahead_ok);
+    float d[J], x[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) x[j] = j * kLanes + lane < a.E ? ahead[j] : -INFINITY;
+    const int id = ahead_id;
+    const bool picked = id >= 0 && id < a.E;
+    const float dw = picked ? ahead_dw : 0.0f;
+    if (t + step < a.S) fetch(t + step);
+    if (ok == 0) {
 #pragma unroll
       for (int j = 0; j < J; ++j) d[j] = 0.0f;
     } else {
-      float s[J], x[J];
-      uint32_t m = 0;
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        const int e = j * kLanes + lane;
-        x[j] = e < a.E ? load_logit<BF16>(a.logits, at + e) : -INFINITY;
-        lds[w][e] = 0.0f;
-        if (e < a.E) m = max(m, order_key(x[j]));
-      }
-      float shift = 0.0f;
+      float s[J], shift = 0.0f;
       if (!a.sigmoid) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const uint32_t k = order_key(x[j]);
+          m = max(m, j * kLanes + lane < a.E ? k : 0u);
+        }
         m = wave_max_u32(m);
         const float top = key_value(m);
         shift = m == 1u || top == -INFINITY ? 0.0f : top;
@@ -507,14 +528,15 @@ __global__ void __launch_bounds__(256) k_route_grad(RouteGradArgs a, int nblk) {
       total = wave_sum(total);
       const float inv = reciprocal_or_zero(total);
       if (a.d_weights != nullptr) {
-        const int id = lane < a.K ? a.topk[tok * a.K + lane] : -1;
-        const bool ok = id >= 0 && id < a.E;
-        const float dw = ok ? a.d_weights[tok * a.K + lane] : 0.0f;
-        float sel = 0.0f;
-        if (ok) {
-          const float v = load_logit<BF16>(a.logits, at + id);
-          sel = a.sigmoid ? logistic(v) : exp_shifted(v, shift);
-        }
+        // scores by id, then the gradients that go to them
+        float* const at_id = lds[w];
+#pragma unroll
+        for (int j = 0; j < J; ++j) at_id[j * kLanes + lane] = s[j];
+        wave_lds_sync();
+        const float sel = picked ? at_id[id] : 0.0f;
+        wave_lds_sync();
+#pragma unroll
+        for (int j = 0; j < J; ++j) at_id[j * kLanes + lane] = 0.0f;
         float g;
         if (a.renorm) {
           const float rn = reciprocal_or_zero(wave_sum(sel));
@@ -523,27 +545,30 @@ __global__ void __launch_bounds__(256) k_route_grad(RouteGradArgs a, int nblk) {
         } else {
           g = a.scale * dw;
         }
-        // softmax scores are total times the ones above: dL/ds of those
+        // softmax scores are inv times the ones above
         if (!a.sigmoid && !a.renorm) g *= inv;
         wave_lds_sync();
-        if (ok) atomicAdd(&lds[w][id], g);
+        if (picked) atomicAdd(&at_id[id], g);
+        wave_lds_sync();
+#pragma unroll
+        for (int j = 0; j < J; ++j) d[j] = at_id[j * kLanes + lane];
+        wave_lds_sync();
+      } else {
+#pragma unroll
+        for (int j = 0; j < J; ++j) d[j] = 0.0f;
       }
-      wave_lds_sync();
-      // s, total and G now go by unnormalised scores; p = s * inv
+      // d is dL/ds of the scores s here, p = s * inv
       float dot = 0.0f;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        const float g = lds[w][j * kLanes + lane];
-        d[j] = g;
-        dot += a.sigmoid ? s[j] * inv * b[j] : s[j] * g + s[j] * inv * b[j];
+        dot = fmaf(s[j] * inv, b[j], dot);
+        if (!a.sigmoid) dot = fmaf(s[j], d[j], dot);
       }
       dot = wave_sum(dot);
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        if (a.sigmoid)
-          d[j] = s[j] * logistic(-x[j]) * (d[j] + (b[j] - dot) * inv);
-        else
-          d[j] = s[j] * (d[j] + (b[j] - dot) * inv);
+        const float ds = d[j] + (b[j] - dot) * inv;
+        d[j] = (a.sigmoid ? s[j] * logistic(-x[j]) : s[j]) * ds;
       }
     }
 #pragma unroll
