@@ -358,16 +358,21 @@ def _dtype_code(t, name):
     return _DTYPES[t.dtype]
 
 
+# The raw handle of a device's current stream without building a Stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _call(dev, fn, *args, stream=None):
     """Calls the library with `dev` current (switching to it and back if it is not)."""
-    f = getattr(_lib, fn)
+    s = _raw_stream(dev) if stream is None else stream.cuda_stream
     if torch.cuda.current_device() == dev:
-        st = f(*args, (stream or torch.cuda.current_stream()).cuda_stream)
+        st = fn(*args, s)
     else:
         with torch.cuda.device(dev):
-            st = f(*args, (stream or torch.cuda.current_stream()).cuda_stream)
+            st = fn(*args, s)
     if st != MOON_OK:
-        raise MoonError(st, fn)
+        raise MoonError(st, fn.__name__)
 
 
 def _groups(plan, rows, dev):
@@ -430,7 +435,7 @@ def moon_route(logits, topk, weights, flags=0, scale=1.0, bias=None, valid=None,
             if stream is not None:
                 workspace.record_stream(stream)
     ws_bytes = 0 if workspace is None else workspace.numel()
-    _call(dev, "moon_route", ctypes.byref(cfg), _addr(logits, logits.dtype, R * S * E, "logits", dev),
+    _call(dev, _lib.moon_route, ctypes.byref(cfg), _addr(logits, logits.dtype, R * S * E, "logits", dev),
           _opt(bias, f32, E, "bias", dev), _flags8(valid, R * S, dev),
           _addr(topk, i32, R * S * K, "topk", dev), _addr(weights, f32, R * S * K, "weights", dev),
           _opt(tokens_per_expert, i32, R * E, "tokens_per_expert", dev),
@@ -457,7 +462,7 @@ def moon_route_backward(logits, topk, d_logits, flags=0, scale=1.0, valid=None, 
     cfg = _route_config(logits, topk.shape[2], flags, scale, loss_coef)
     R, S, E, K = cfg.R, cfg.S, cfg.E, cfg.K
     dev, i32, f32 = _device_of(logits, "logits"), torch.int32, torch.float32
-    _call(dev, "moon_route_backward", ctypes.byref(cfg),
+    _call(dev, _lib.moon_route_backward, ctypes.byref(cfg),
           _addr(logits, logits.dtype, R * S * E, "logits", dev), _flags8(valid, R * S, dev),
           _addr(topk, i32, R * S * K, "topk", dev),
           _opt(d_weights, f32, R * S * K, "d_weights", dev),
@@ -477,7 +482,7 @@ def _mx4_call(fn, x, q, scales, plan, stream):
     pq = _addr(q, torch.uint8, rows * (cols // 2), "q", dev)
     ps = _addr(scales, torch.uint8, rows * (cols // 32), "scales", dev)
     code = _dtype_code(x, "values")
-    if fn == "moon_mx4_quantize":
+    if fn is _lib.moon_mx4_quantize:
         _call(dev, fn, px, code, rows, cols, pa, pq, ps, stream=stream)
     else:
         _call(dev, fn, pq, ps, rows, cols, pa, code, px, stream=stream)
@@ -486,12 +491,12 @@ def _mx4_call(fn, x, q, scales, plan, stream):
 def moon_mx4_quantize(x, q, scales, plan=None, stream=None):
     """x [..., cols] (float32 or bfloat16) to MXFP4 codes q [..., cols/2] and
     scales [..., cols/32] (uint8).  With a plan x is window rows [R*NvS, cols]."""
-    _mx4_call("moon_mx4_quantize", x, q, scales, plan, stream)
+    _mx4_call(_lib.moon_mx4_quantize, x, q, scales, plan, stream)
 
 
 def moon_mx4_dequantize(q, scales, y, plan=None, stream=None):
     """The values of MXFP4 codes and scales, to y [..., cols]."""
-    _mx4_call("moon_mx4_dequantize", y, q, scales, plan, stream)
+    _mx4_call(_lib.moon_mx4_dequantize, y, q, scales, plan, stream)
 
 
 def _mx4_weight(pa, w, N, K, name, dev):
@@ -518,7 +523,7 @@ def moon_expert_gemm_mx4(plan, xq, xs, weight, y, stream=None):
     N, K, dev = _rows_of(y, "y")[1], 2 * half, _device_of(xq, "xq")
     pa = _groups(plan, rows, dev)
     w = _mx4_weight(pa, weight, N, K, "weight", dev)
-    _call(dev, "moon_expert_gemm_mx4", ctypes.byref(pa),
+    _call(dev, _lib.moon_expert_gemm_mx4, ctypes.byref(pa),
           _addr(xq, torch.uint8, rows * half, "xq", dev),
           _addr(xs, torch.uint8, rows * (K // 32), "xs", dev), K, ctypes.byref(w), N,
           _addr(y, torch.bfloat16, rows * N, "y", dev), stream=stream)
@@ -532,7 +537,7 @@ def moon_expert_swiglu_mx4(plan, xq, xs, gate, up, h, row_weights=None, stream=N
     pa = _groups(plan, rows, dev)
     wg = _mx4_weight(pa, gate, F, K, "gate", dev)
     wu = _mx4_weight(pa, up, F, K, "up", dev)
-    _call(dev, "moon_expert_swiglu_mx4", ctypes.byref(pa),
+    _call(dev, _lib.moon_expert_swiglu_mx4, ctypes.byref(pa),
           _addr(xq, torch.uint8, rows * half, "xq", dev),
           _addr(xs, torch.uint8, rows * (K // 32), "xs", dev), K, ctypes.byref(wg),
           ctypes.byref(wu), F, _opt(row_weights, torch.float32, rows, "row_weights", dev),
@@ -546,7 +551,7 @@ def moon_swiglu_save8(plan, gate_up, h, saved, saved_scales, row_weights=None, s
     rows, F = _rows_of(h, "h")
     dev = _device_of(h, "h")
     pa = _groups(plan, rows, dev)
-    _call(dev, "moon_swiglu_save8", ctypes.byref(pa),
+    _call(dev, _lib.moon_swiglu_save8, ctypes.byref(pa),
           _addr(gate_up, torch.bfloat16, rows * 2 * F, "gate_up", dev),
           _opt(row_weights, torch.float32, rows, "row_weights", dev), F,
           _addr(h, torch.bfloat16, rows * F, "h", dev),
@@ -562,7 +567,7 @@ def moon_swiglu_grad8(plan, dh, saved, saved_scales, d_gate_up, row_weights=None
     rows, F = _rows_of(dh, "dh")
     dev = _device_of(dh, "dh")
     pa = _groups(plan, rows, dev)
-    _call(dev, "moon_swiglu_grad8", ctypes.byref(pa),
+    _call(dev, _lib.moon_swiglu_grad8, ctypes.byref(pa),
           _addr(dh, torch.bfloat16, rows * F, "dh", dev),
           _addr(saved, torch.uint8, rows * 2 * F, "saved", dev),
           _addr(saved_scales, torch.uint8, rows * (2 * F // 32), "saved_scales", dev),
