@@ -427,7 +427,7 @@ def moon_route(logits, topk, weights, flags=0, scale=1.0, bias=None, valid=None,
     cfg = _route_config(logits, topk.shape[2], flags, scale, loss_coef)
     R, S, E, K = cfg.R, cfg.S, cfg.E, cfg.K
     dev, i32, f32 = _device_of(logits, "logits"), torch.int32, torch.float32
-    if workspace is None and S > 256 and not (tokens_per_expert is None and valid_tokens is None
+    if workspace is None and S > 32 and not (tokens_per_expert is None and valid_tokens is None
                                               and prob_sums is None and loss is None):
         n = moon_route_workspace(R, S, E, K)
         if n > 0:

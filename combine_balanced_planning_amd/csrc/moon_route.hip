@@ -587,13 +587,16 @@ __global__ void __launch_bounds__(256) k_route_grad(RouteGradArgs a, int nblk) {
   }
 }
 
-// How a call is cut: waves per workgroup and workgroups per rank.  Up to 256
-// tokens a rank one workgroup of 16 waves does it all in one launch; beyond
-// that workgroups of eight waves, four to a compute unit (1024 in all), and a
-// second launch adds their partial sums.  Without counts, sums or loss there
-// is nothing to add and every four tokens get a workgroup.
+// How a call is cut: waves per workgroup and workgroups per rank.  Up to 32
+// tokens a rank one workgroup of 16 waves does it all in one launch, at most
+// two tokens a wave of about 3.5 us each; beyond that workgroups of eight
+// waves, four to a compute unit (1024 in all), and a second launch of about
+// 6 us adds their partial sums.  Without counts, sums or loss there is nothing
+// to add and every four tokens get a workgroup.
+constexpr int kOneLaunchTokens = 32;
+
 void route_cut(int R, int S, bool stats, int* waves, int* nblk) {
-  if (stats && S <= 256) {
+  if (stats && S <= kOneLaunchTokens) {
     *waves = std::min(kMaxWaves, S);
     *nblk = 1;
     return;
