@@ -6,14 +6,14 @@
 //                       with the gate and the up weights of f
 // for every row of every group g of every rank, W_g the weights of the group's
 // expert (a rank's own experts, or the prefetched copy in the group's slot).
-// Values and scales go into the matrix cores as they are stored: one
-// v_mfma_scale_f32_16x16x128 multiplies 16 weight rows by 16 window rows over
-// 128 values, each lane holding the 32 values of one scale block, exact
-// products summed in fp32.  The result is rounded once, to bf16.
+// Values and scales go into the matrix cores as they are stored: a
+// v_mfma_scale_f32 takes 32 values of a row and their scale per lane, and sums
+// exact products in fp32.  The result is rounded once, to bf16.  The weights are
+// the operand whose rows land in a lane's registers, so a lane owns
+// neighbouring outputs of one window row.
 //
-// The weights are the matrix operand whose rows land in a lane's four
-// registers, so a lane owns four neighbouring outputs of one window row and
-// stores them as one 8-byte word.
+// Two kernels: one streams the weights past a few rows, the other multiplies
+// tiles of 256 by 256.
 #include <algorithm>
 
 #include "moon_rows.h"
@@ -367,6 +367,15 @@ __device__ __forceinline__ void half_step(const vec4u* wsrc, const vec4u* xsrc, 
 // twice.  Each step refills the buffer it has just emptied with the same step
 // of the next turn, which may belong to the next tile: the loads run three
 // steps ahead without a pause at tile borders.
+//
+// Gate and up products of 262144 rows, K=7168, F=2048 in 288 groups take 4.25 ms
+// (3.6 PFLOP/s, 4.1 with the unused rows of the groups' last tiles) at a clock
+// that the power limit holds near 1.65 GHz; a library's product of two 16384 x
+// 16384 MXFP4 matrices reaches 3.2 PFLOP/s on the same card.  Tried and slower:
+// four waves of 128 by 128 (256 accumulators: spills, or waits that drain the
+// loads), 128 bytes of a row a load with two steps ahead, loads into the caches
+// further ahead, a raised wave priority, leaving out the products of rows that
+// a last tile lacks.
 template <bool Swiglu, bool Whole>
 __global__ void __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
     k_expert_tiles(ExpertArgs a, Groups g) {
@@ -420,27 +429,23 @@ __global__ void __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_
   int t_load = (int)((int64_t)total * xcd / 8) + (int)(blockIdx.x >> 3);
   if (t_load >= t_end) return;
 
+  // Tile t, which is never before the one asked for last: its entry is looked
+  // for from there on.
+  int entry = 0;
   const auto find = [&](int t) {
     const int mt = t / nt;
-    int lo = 0, hi = entries;  // first[lo] <= mt < first[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (first[mid] <= mt)
-        lo = mid;
-      else
-        hi = mid;
-    }
+    while (first[entry + 1] <= mt) ++entry;
+    entry = uniform(entry);
+    const int before = uniform(first[entry]), m_tiles = uniform(first[entry + 1]) - before;
+    const int in = t - before * nt, n = in / m_tiles, m = in - n * m_tiles;
+    const Span sp = group_span(g, entry / g.per, entry % g.per);
     Tile o;
-    const int m_tiles = first[lo + 1] - first[lo];
-    const int in = t - first[lo] * nt;
-    const int m = in % m_tiles;
-    const Span sp = group_span(g, lo / g.per, lo % g.per);
-    o.u = uniform(lo / g.per);
-    o.j = uniform(lo % g.per);
-    o.n0 = uniform(in / m_tiles * kOut);
-    o.row0 = uniform(sp.begin + m * kTile);
-    o.rows = uniform(sp.real_end - (sp.begin + m * kTile));
-    o.pad = uniform(m == m_tiles - 1 ? sp.end - sp.real_end : 0);
+    o.u = entry / g.per;
+    o.j = entry % g.per;
+    o.n0 = n * kOut;
+    o.row0 = sp.begin + m * kTile;
+    o.rows = sp.real_end - o.row0;
+    o.pad = m == m_tiles - 1 ? sp.end - sp.real_end : 0;
     return o;
   };
 
@@ -460,7 +465,10 @@ __global__ void __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_
     return (Swiglu ? (f >> 2) * 64 + (f & 1) * 32 : f * 32) + h * 16 + r;
   };
   const uint32_t row_bytes = 16u * blocks;
-  const auto point = [&](const Tile& t) {
+  const auto point = [&](Tile& t) {
+    t.row0 = uniform(t.row0);
+    t.rows = uniform(t.rows);
+    t.pad = uniform(t.pad);
     const uint8_t *wq[2], *ws[2];
     weight_of(g, a.w[0], t.u, t.j, a.N, a.K, &wq[0], &ws[0]);
     weight_of(g, a.w[Swiglu ? 1 : 0], t.u, t.j, a.N, a.K, &wq[1], &ws[1]);
@@ -565,7 +573,18 @@ __global__ void __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_
         s[h][i] = sc[b][(i < 4 ? wfrag : xfrag) + scale_in + (i & 3) * 2 * kLanes + 32 * h];
   };
 
-  Tile cur = find(t_load), next = cur;
+  {  // the first tile's entry, by halves
+    const int mt = t_load / nt;
+    int hi = entries;  // first[entry] <= mt < first[hi]
+    while (hi - entry > 1) {
+      const int mid = (entry + hi) / 2;
+      if (first[mid] <= mt)
+        entry = mid;
+      else
+        hi = mid;
+    }
+  }
+  Tile cur = find(t_load), next;
   point(cur);
   {
     vec4u v = {};
@@ -585,7 +604,7 @@ __global__ void __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_
     fa[i] = st0[(i < 4 ? wfrag : xfrag) + in0 + (i & 3) * 2 * kLanes];
   read_scales(0, 0, sr);
   int buf = 0;
-  bool more = true;  // a turn is left to load
+  bool more = true;  // a tile is left to load
   while (true) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -593,6 +612,12 @@ __global__ void __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_
       for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][k][r] = 0.0f;
+    // The next tile is looked up now, so that what it needs from memory is here
+    // when its loads begin.
+    t_load += xn;
+    more = t_load < t_end;
+    next = cur;
+    if (more) next = find(t_load);
 #pragma unroll 1
     for (int turn = 0; turn < turns; ++turn) {
       // The turn to load: the next of this tile, or the first of the next
@@ -600,12 +625,7 @@ __global__ void __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_
       int turn_load = turn + 1;
       if (turn_load == turns) {
         turn_load = 0;
-        t_load += xn;
-        more = t_load < t_end;
-        if (more) {
-          next = find(t_load);
-          point(next);
-        }
+        if (more) point(next);
       }
       vec4u v = {};
       if (!Whole) v = get_scales(turn_load);
@@ -670,7 +690,7 @@ __global__ void __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_
           v[q] = vec4u{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
                        pack_bf16(o[6], o[7])};
         }
-        const int c = col + 32 * i + out_col;
+        vec4u p[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           if (((lane >> 4) & 1) == j) {
@@ -678,12 +698,15 @@ __global__ void __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_
             put[(2 * half + 1) ^ swap] = v[1];
           }
           wave_lds_sync();
-          const vec4u p = turned[w][lane];
+          p[j] = turned[w][lane];
           wave_lds_sync();
-          const int r = m + 16 * j + out_row;
-          if (r < cur.rows && c < a.N) *reinterpret_cast<vec4u*>(a.y + (base + r) * a.N + c) = p;
         }
-        __builtin_amdgcn_sched_barrier(0);
+        const int c = col + 32 * i + out_col;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int r = m + 16 * j + out_row;
+          if (r < cur.rows && c < a.N) *reinterpret_cast<vec4u*>(a.y + (base + r) * a.N + c) = p[j];
+        }
       }
     }
     zero_rows(a.y, base + cur.rows, cur.pad, a.N, cur.n0, kOut);
@@ -712,8 +735,13 @@ moon_status check(const ExpertArgs& a, const moon_plan_arrays* plan, int product
 
 template <bool Swiglu>
 moon_status launch(const ExpertArgs& a, const Groups& g, hipStream_t s) {
+  // By the rows an expert gets on average, over K=2048, N=7168, E=256 (R=8, 288
+  // groups; us by 16 rows at a time, by 64 and by tiles of 256):
+  //   2 rows 320/367/415, 8 rows 420/472/537, 16 rows 477/474/550,
+  //   32 rows 663/513/578, 64 rows 1107/647/591, 128 rows 2087/1041/667.
+  // The counts themselves are on the GPU; any group is right in any kernel.
   const int64_t rows = (int64_t)g.R * g.N;
-  if (rows >= 96 * (int64_t)g.E && g.R * g.per <= kMaxEntries) {
+  if (rows >= 48 * (int64_t)g.E && g.R * g.per <= kMaxEntries) {
     int dev = 0, cus = 256;
     if (hipGetDevice(&dev) == hipSuccess)
       (void)hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
@@ -724,10 +752,8 @@ moon_status launch(const ExpertArgs& a, const Groups& g, hipStream_t s) {
       hipLaunchKernelGGL((k_expert_tiles<Swiglu, false>), dim3(wgs), dim3(kTileThreads), 0, s, a, g);
     return hipGetLastError() == hipSuccess ? MOON_OK : MOON_ERR_HIP;
   }
-  // Up to eight rows a group on average: 16 at a time hold nearly every group;
-  // beyond that 64, so that a group's weights are read once.
   const dim3 grid(Swiglu ? (a.N + 31) / 32 : (a.N + 63) / 64, g.R * g.per);
-  const bool few = rows <= 8 * (int64_t)g.E;
+  const bool few = rows <= 12 * (int64_t)g.E;
   if (a.K % 512 == 0) {
     if (few)
       hipLaunchKernelGGL((k_expert_stream<1, Swiglu, true>), grid, dim3(256), 0, s, a, g);
