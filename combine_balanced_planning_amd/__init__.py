@@ -430,10 +430,9 @@ def moon_route(logits, topk, weights, flags=0, scale=1.0, bias=None, valid=None,
     if workspace is None and S > 32 and not (tokens_per_expert is None and valid_tokens is None
                                               and prob_sums is None and loss is None):
         n = moon_route_workspace(R, S, E, K)
-        if n > 0:
-            workspace = torch.empty(n, dtype=torch.uint8, device=logits.device)
-            if stream is not None:
-                workspace.record_stream(stream)
+        if n > 0:  # from the pool of the stream that uses it, so nothing else still does
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(n, dtype=torch.uint8, device=logits.device)
     ws_bytes = 0 if workspace is None else workspace.numel()
     _call(dev, _lib.moon_route, ctypes.byref(cfg), _addr(logits, logits.dtype, R * S * E, "logits", dev),
           _opt(bias, f32, E, "bias", dev), _flags8(valid, R * S, dev),

@@ -69,7 +69,7 @@ __device__ __forceinline__ void zero_rows(uint16_t* y, int64_t row0, int rows, i
                                           int width) {
   const int vecs = min(width, N - n0) / 8;
   const vec4u zero = {0u, 0u, 0u, 0u};
-  for (int i = threadIdx.x; i < rows * vecs; i += blockDim.x)
+  for (int64_t i = threadIdx.x; i < (int64_t)rows * vecs; i += blockDim.x)
     *reinterpret_cast<vec4u*>(y + (row0 + i / vecs) * N + n0 + i % vecs * 8) = zero;
 }
 

@@ -164,18 +164,51 @@ def test_lane_layout(env):
     assert (y[:64] == want).all()
 
 
-def test_nan_scales_reach_their_outputs_only(env):
+@pytest.mark.parametrize("rows", [(40, 20), (300, 260), (3, 2)])
+@pytest.mark.parametrize("K", [320, 512])
+def test_nan_scales_reach_their_outputs_only(env, rows, K):
     """A NaN block of one row or one weight row makes that row's or column's
     outputs NaN and no others."""
-    c = Case(env, own(1, 2, 1, [40, 20]), 2, 1, 320, 48, seed=2)
-    c.xs[7, 3] = 255
+    c = Case(env, own(1, 2, 1, rows), 2, 1, K, 48, seed=2)
+    c.xs[rows[0] - 1, 3] = 255
     c.ws[0][1][1, 33, 9] = 255
     y = c.run(env, False)
     bad = np.zeros(y.shape, bool)
-    bad[7] = True
-    bad[40:60, 33] = True
-    bad[c.kind == 0] = False
+    bad[rows[0] - 1] = True
+    bad[rows[0]:sum(rows), 33] = True
     assert (np.isnan(y) == bad).all()
+
+
+@pytest.mark.parametrize("rows", [(5, 20), (300, 130)])
+@pytest.mark.parametrize("up,down", [(250, 4), (4, 250), (254, 0), (0, 254)])
+def test_scales_at_their_ends(env, rows, up, down):
+    """Scales of 2^123 against 2^-123, and of 2^127 against 2^-127: the products
+    are ordinary numbers, and stay exact."""
+    c = Case(env, own(1, 2, 1, rows), 2, 1, 544, 40, seed=6)
+    c.xs[c.kind == 1] = up
+    for a in c.ws[0][1::2]:
+        a[:] = down
+    y, mag = c.products(c.ws[0])
+    c.check_rows(c.run(env, False), y, c.K * 2.0 ** -23 * mag)
+
+
+def test_rows_beyond_32_bit_offsets(env):
+    """A window of 2.4e9 outputs (4.8 GB): rows at both ends of it."""
+    moon, torch, dev = env
+    K, N, rows = 64, 8192, 300000
+    arrays, NvS = ref.plan_arrays([[rows - 7, 5, 0]], 2, 1)
+    plan = {k: torch.from_numpy(v).to(dev) for k, v in arrays.items()}
+    g = torch.Generator(device=dev).manual_seed(1)
+    rnd = lambda lo, hi, *n: torch.randint(lo, hi, n, generator=g, device=dev, dtype=torch.uint8)  # noqa: E731
+    xq, xs = rnd(0, 255, NvS, K // 2), rnd(124, 129, NvS, K // 32)
+    w = (rnd(0, 255, 2, N, K // 2), rnd(120, 125, 2, N, K // 32), rnd(0, 255, 1, 1, N, K // 2),
+         rnd(120, 125, 1, 1, N, K // 32))
+    y = torch.full((NvS, N), 77.0, dtype=torch.bfloat16, device=dev)
+    moon.moon_expert_gemm_mx4(plan, xq, xs, w, y)
+    values = lambda q, s: ref.mx4_values(q.cpu().numpy(), s.cpu().numpy())  # noqa: E731
+    for at, e in ((slice(0, 9), 0), (slice(rows - 20, rows - 7), 0), (slice(rows - 7, rows - 2), 1)):
+        x, v = values(xq[at], xs[at]), values(w[0][e], w[1][e])
+        close(y[at].double().cpu().numpy(), x @ v.T, K * 2.0 ** -23 * (np.abs(x) @ np.abs(v).T))
 
 
 def test_failed_plan_writes_nothing(env):

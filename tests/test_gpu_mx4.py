@@ -146,6 +146,42 @@ def test_planned_rows(env, i, cols):
     assert (q == 0xEE).all() and (s == 0xEE).all() and (y == 77).all()
 
 
+@pytest.mark.parametrize("planned", [False, True])
+def test_rows_beyond_32_bit_offsets(env, planned):
+    """2.4e9 values (4.8 GB of bf16): rows at both ends."""
+    moon, torch, dev = env
+    rows, cols = 300000, 8192
+    plan = None
+    if planned:
+        arrays, rows = ref.plan_arrays([[rows, 0]], 1, 1)
+        plan = {k: torch.from_numpy(v).to(dev) for k, v in arrays.items()}
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev).normal_(generator=torch.Generator(device=dev).manual_seed(2))
+    q = torch.zeros((rows, cols // 2), dtype=torch.uint8, device=dev)
+    s = torch.zeros((rows, cols // 32), dtype=torch.uint8, device=dev)
+    y = torch.zeros_like(x)
+    moon.moon_mx4_quantize(x, q, s, plan=plan)
+    moon.moon_mx4_dequantize(q, s, y, plan=plan)
+    for at in (slice(0, 3), slice(rows - 5, rows)):
+        wq, ws = ref.mx4(x[at].double().cpu().numpy())
+        assert (q[at].cpu().numpy() == wq).all() and (s[at].cpu().numpy() == ws).all()
+        assert same(y[at].double().cpu().numpy(), ref.mx4_values(wq, ws))
+
+
+def test_scales_off_their_words(env):
+    """Scale bytes may start anywhere; rows of 128 values and more store them
+    four at a time only where they lie on whole words."""
+    moon, torch, dev = env
+    x = torch.randn((37, 256), device=dev).bfloat16()
+    q = torch.zeros((37, 128), dtype=torch.uint8, device=dev)
+    wq, ws = ref.mx4(x.double().cpu().numpy())
+    for off in (1, 2, 3, 4):
+        buf = torch.full((37 * 8 + 8,), 0xEE, dtype=torch.uint8, device=dev)
+        s = buf[off:off + 37 * 8].view(37, 8)
+        moon.moon_mx4_quantize(x, q, s)
+        assert (s.cpu().numpy() == ws).all() and (q.cpu().numpy() == wq).all()
+        assert (buf[:off] == 0xEE).all() and (buf[off + 37 * 8:] == 0xEE).all()
+
+
 def test_weights_of_three_axes_and_graph(env):
     """[E, N, K] weights in one call; captured and replayed on new values."""
     moon, torch, dev = env

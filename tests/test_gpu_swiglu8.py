@@ -164,6 +164,30 @@ def test_gradient_against_differences(env):
         assert abs((f(x, up) - f(x, dn)) / 2e-4 - dw[r]) < 1e-4
 
 
+def test_rows_beyond_32_bit_offsets(env):
+    """Gate and up of 2.6e9 values (5.2 GB): the last rows are their own
+    activation and gradient."""
+    moon, torch, dev = env
+    F, rows = 4096, 320000
+    arrays, NvS = ref.plan_arrays([[rows - 9, 9, 0]], 2, 1)
+    plan = {k: torch.from_numpy(v).to(dev) for k, v in arrays.items()}
+    g = torch.Generator(device=dev).manual_seed(4)
+    x = torch.empty((NvS, 2 * F), dtype=torch.bfloat16, device=dev).normal_(generator=g)
+    dh = torch.empty((NvS, F), dtype=torch.bfloat16, device=dev).normal_(generator=g)
+    o = step(env, plan, x, dh, None, F)
+    for at in (slice(0, 2), slice(rows - 3, rows)):
+        xv, d = x[at].double().cpu().numpy(), dh[at].double().cpu().numpy()
+        h = ref.silu(xv[:, :F]) * xv[:, F:]
+        assert (np.abs(o["h"][at].double().cpu().numpy() - h) <= (2.0 ** -8 + 16 * EPS) * np.abs(h) + 1e-37).all()
+        s = ref.mx_scale(xv, 8)
+        codes = ref.mx_codes(xv, s, 8)
+        assert (o["saved"][at].cpu().numpy() == codes).all() and (o["scales"][at].cpu().numpy() == s).all()
+        v = ref.mx_values(codes, s, 8)
+        du = d * ref.silu(v[:, :F])
+        assert (np.abs(o["dx"][at].double().cpu().numpy()[:, F:] - du) <= 2.0 ** -8 * np.abs(du) +
+                32 * EPS * np.abs(d * v[:, :F]) + 1e-37).all()
+
+
 def test_without_weight_gradient_failed_plan_and_graph(env):
     moon, torch, dev = env
     plan, x, dh, w = check(env, [[33, 0, 9], [0, 20, 0]], 2, 8, 160, True, seed=8)
