@@ -15,11 +15,15 @@
 //
 // One wave per token, lane l holds experts l, l + 64, ...: the logits are
 // read once, coalesced, and everything else stays in registers.  The K-th
-// largest of the lanes' maxima bounds the K-th largest key from below; bisection
-// of its bits with a ballot a round finds it.  The keys that reach it, K and a
-// few more, are packed into lanes and ranked by comparing all pairs.  Sums over tokens are kept per wave in
-// registers, then per workgroup in LDS, then per workgroup in the workspace,
-// and added in a fixed order at each step, so results repeat bit for bit.
+// largest of the lanes' maxima bounds the K-th largest value from below; bisection
+// of its bits with a ballot a round finds it.  The values that reach it, K and a
+// few more, are packed into lanes and ranked by comparing all pairs.  All but
+// the maxima and the picks are compared as the numbers they are: an integer key
+// for every expert took a third more vector instructions (44 against 39 us a
+// call at R=8, S=4096, E=256 with a bias).
+// Sums over tokens are kept per wave in registers, then per workgroup in LDS,
+// then per workgroup in the workspace, and added in a fixed order at each step,
+// so results repeat bit for bit.
 #include <algorithm>
 
 #include "moon_rows.h"
@@ -30,6 +34,7 @@ namespace {
 constexpr int kMaxWaves = 16;
 constexpr int kMaxExperts = 512;
 constexpr int kMaxTopk = 64;
+enum { kSoftmax, kSigmoid, kBiased };
 
 struct RouteArgs {
   const void* logits;
@@ -43,7 +48,7 @@ struct RouteArgs {
   int32_t* part_c;  // [R][nblk][E]
   int32_t* part_n;  // [R][nblk]
   int32_t R, S, E, K, nblk;
-  int32_t sigmoid, renorm, stats;
+  int32_t sigmoid, renorm, stats, sums;
   float scale, coef;
 };
 
@@ -92,9 +97,10 @@ __device__ __forceinline__ int count_at_least(const uint32_t (&key)[J], uint32_t
   return n;
 }
 
-__device__ __forceinline__ int lanes_before(uint64_t ballot) {
+// `first` plus the lanes of the ballot below this one.
+__device__ __forceinline__ int lanes_before(uint64_t ballot, int first = 0) {
   return __builtin_amdgcn_mbcnt_hi((uint32_t)(ballot >> 32),
-                                   __builtin_amdgcn_mbcnt_lo((uint32_t)ballot, 0));
+                                   __builtin_amdgcn_mbcnt_lo((uint32_t)ballot, first));
 }
 
 // A key and its expert as one number: larger keys first, then lower ids.
@@ -103,6 +109,10 @@ __device__ __forceinline__ uint64_t pick_of(uint32_t key, int id) {
 }
 __device__ __forceinline__ uint32_t pick_key(uint64_t p) { return (uint32_t)(p >> 32); }
 __device__ __forceinline__ int pick_id(uint64_t p) { return (int)~(uint32_t)p; }
+
+__device__ __forceinline__ float read_lane(float v, int lane) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
+}
 
 template <bool BF16>
 __device__ __forceinline__ float load_logit(const void* base, int64_t i) {
@@ -200,32 +210,39 @@ __device__ __forceinline__ void finish_rank(const RouteArgs& a, int r, int n, fl
 }
 
 // Held to 64 registers for eight waves a SIMD: a token is a chain of dependent
-// steps, and more waves hide it (113 -> 96 us at R=16, S=8192, E=384).
-template <int J, bool BF16>
+// steps, and more waves hide it (an earlier version took 113 us with fewer and
+// 96 with eight).  What selects, whether sums over tokens (or a token's sum of
+// scores) are wanted and whether the words are full are template arguments:
+// told at run time they cost branches and spilled scalars, 96 against 73 us a
+// call at R=16, S=8192, E=384, fp32.  There a token takes 233 vector and 184
+// scalar instructions, the kernel 67 us with the vector unit busy 70 % of
+// them; the logits alone take 41 us to read.
+template <int J, bool BF16, int Score, bool Sums, bool Whole>
 __global__ void __launch_bounds__(kMaxWaves* kLanes) __attribute__((amdgpu_waves_per_eu(8)))
     k_route(RouteArgs a) {
-  extern __shared__ float lds[];  // [waves][64] picks; with stats also [waves][E] sums,
-                                  // [E] counts, [waves] tokens, [waves]
+  constexpr bool biased = Score == kBiased, sigmoid = Score != kSoftmax;
+  const int E = Whole ? J * kLanes : a.E;  // Whole: the words are full
+  extern __shared__ float lds[];  // [waves][64] picks; with stats also [E] counts,
+                                  // [waves] tokens, [waves]; with Sums [waves][E] sums
   const int lane = threadIdx.x & (kLanes - 1);
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
   const int waves = blockDim.x / kLanes;
   const int r = blockIdx.y, blk = blockIdx.x;
   uint64_t* const picks = reinterpret_cast<uint64_t*>(lds) + w * kLanes;
-  float* const red_p = lds + 2 * waves * kLanes;
-  int32_t* const red_c = reinterpret_cast<int32_t*>(red_p + waves * a.E);
-  int32_t* const red_n = red_c + a.E;
+  int32_t* const red_c = reinterpret_cast<int32_t*>(lds + 2 * waves * kLanes);
+  int32_t* const red_n = red_c + E;
   float* const red_l = reinterpret_cast<float*>(red_n + waves);
+  float* const red_p = red_l + waves;
   if (a.stats) {
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x) red_c[e] = 0;
+    for (int e = threadIdx.x; e < E; e += blockDim.x) red_c[e] = 0;
     __syncthreads();
   }
-  const bool biased = a.bias != nullptr;
   float acc[J], bias[J];
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int e = j * kLanes + lane;
     acc[j] = 0.0f;
-    bias[j] = biased && e < a.E ? a.bias[e] : 0.0f;
+    bias[j] = biased && e < E ? a.bias[e] : 0.0f;
   }
   int32_t n_valid = 0;
   // The next token's logits are on their way while one is worked on.
@@ -235,22 +252,24 @@ __global__ void __launch_bounds__(kMaxWaves* kLanes) __attribute__((amdgpu_waves
   const auto fetch = [&](int t) {
     const int64_t tok = (int64_t)r * a.S + t;
     if (a.valid != nullptr) ahead_ok = a.valid[tok];
+    const void* const row = static_cast<const char*>(a.logits) + tok * E * (BF16 ? 2 : 4);
 #pragma unroll
-    for (int j = 0; j < J; ++j)
-      ahead[j] = load_logit<BF16>(a.logits, tok * a.E + min(j * kLanes + lane, a.E - 1));
+    for (int j = 0; j < J; ++j) {
+      const uint32_t e = j * kLanes + lane;
+      ahead[j] = load_logit<BF16>(row, Whole ? e : min(e, (uint32_t)E - 1));
+    }
   };
   if (blk * waves + w < a.S) fetch(blk * waves + w);
   for (int t = blk * waves + w; t < a.S; t += step) {
     const int64_t tok = (int64_t)r * a.S + t;
-    const int64_t at = tok * a.E;
+    const int64_t at = tok * E;
     const int ok = __builtin_amdgcn_readfirstlane((int)ahead_ok);
-    float s[J];
-    uint32_t key[J];
+    // v: what is selected by, NaN where there is no expert; s: the scores.
+    float s[J], v[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       s[j] = ahead[j];
-      const uint32_t k = order_key(s[j]);
-      key[j] = j * kLanes + lane < a.E ? k : 0u;
+      v[j] = j * kLanes + lane < E ? s[j] : NAN;
     }
     if (t + step < a.S) fetch(t + step);
     if (ok == 0) {
@@ -261,40 +280,38 @@ __global__ void __launch_bounds__(kMaxWaves* kLanes) __attribute__((amdgpu_waves
       continue;
     }
     ++n_valid;
-    if (a.sigmoid && (biased || a.stats)) {
+    if (sigmoid && (biased || Sums)) {
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        const float x = s[j];
-        s[j] = logistic(x);
-        if (biased && key[j] != 0u && x != -INFINITY) key[j] = order_key(s[j] + bias[j]);
+        const float x = v[j];
+        s[j] = logistic(s[j]);
+        if (biased) v[j] = x > -INFINITY ? s[j] + bias[j] : x;
       }
     }
-    uint32_t mine = key[0];
+    // (made quiet first: the three-way maximum would return a signalling NaN)
+    float best = __builtin_canonicalizef(v[0]);
 #pragma unroll
-    for (int j = 1; j < J; ++j) mine = max(mine, key[j]);
+    for (int j = 1; j < J; ++j) best = fmaxf(best, __builtin_canonicalizef(v[j]));
+    const uint32_t mine = lane < E ? order_key(best) : 0u;
     const uint32_t top = wave_max_u32(mine);
-    float shift = 0.0f;
-    if (!a.sigmoid) {
+    // At least K of the lanes' maxima are >= lo (min(E, 64) lanes have one),
+    // fewer than K are >= hi.
+    uint32_t lo = wave_min_u32(mine == 0u ? ~0u : mine), hi = top + 1u;
+    float shift = 0.0f, total = 0.0f;
+    if (!sigmoid) {
       // Nothing but masked experts or NaN: scores 0 (NaN) with no shift.
       const float m = key_value(top);
       shift = top == 1u || m == -INFINITY ? 0.0f : m;
-      if (a.stats || !a.renorm) {
-#pragma unroll
-        for (int j = 0; j < J; ++j) s[j] = exp_shifted(s[j], shift);
-      }
     }
-    float total = 0.0f;
-    if (a.stats || !a.renorm) {
+    if (Sums) {
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        if (j * kLanes + lane >= a.E) s[j] = 0.0f;
+        if (!sigmoid) s[j] = exp_shifted(s[j], shift);
+        if (j * kLanes + lane >= E) s[j] = 0.0f;
         total += s[j];
       }
       total = wave_sum(total);
     }
-    // At least K of the lanes' maxima are >= lo (min(E, 64) lanes have one),
-    // fewer than K are >= hi.
-    uint32_t lo = wave_min_u32(mine == 0u ? ~0u : mine), hi = top + 1u;
     // A few maxima too many cost less than the rounds that would tell them,
     // unless every pair is looked at twice.
     const int enough = biased ? a.K : a.K + (a.K >> 1);
@@ -303,24 +320,36 @@ __global__ void __launch_bounds__(kMaxWaves* kLanes) __attribute__((amdgpu_waves
       const int n = __popcll(__ballot(mine >= mid));
       if (n < a.K) {
         hi = mid;
-      } else {
-        lo = mid;
-        if (n <= enough) break;
+        continue;
       }
+      lo = mid;
+      if (n <= enough) break;
     }
-    int found = count_at_least(key, lo);
-    const bool crowded = found > kLanes;
-    int at_pick = 0;
-    if (!crowded) {
+    // Comparisons of numbers from here: NaN takes no part, so a row that needs
+    // one finds fewer than K.
+    const float least = key_value(lo);
+    uint64_t in[J];
+    int first[J], found = 0;
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
-        const uint64_t b = __ballot(key[j] >= lo);
-        if (key[j] >= lo) picks[at_pick + lanes_before(b)] = pick_of(key[j], j * kLanes + lane);
-        at_pick += __popcll(b);
-      }
+    for (int j = 0; j < J; ++j) {
+      in[j] = __ballot(v[j] >= least);
+      first[j] = found;
+      found += __popcll(in[j]);
+    }
+    const bool plain = found >= a.K && found <= kLanes;
+    if (plain) {
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        if (v[j] >= least)
+          picks[lanes_before(in[j], first[j])] =
+              (uint64_t)__float_as_uint(v[j]) << 32 | (uint32_t)~(j * kLanes + lane);
     } else {
-      // Too many for the lanes (long runs of equal keys): on by all keys, and of
-      // those equal at the end the first ones, as many as there is room for.
+      // Too many for the lanes (large K, long runs of equal keys) or NaN: on by
+      // all keys, and of those equal at the end the first ones, as many as
+      // there is room for.
+      uint32_t key[J];
+#pragma unroll
+      for (int j = 0; j < J; ++j) key[j] = j * kLanes + lane < E ? order_key(v[j]) : 0u;
       hi = top + 1u;
       while (hi - lo > 1u) {
         const uint32_t mid = lo + (hi - lo) / 2;
@@ -331,74 +360,93 @@ __global__ void __launch_bounds__(kMaxWaves* kLanes) __attribute__((amdgpu_waves
       }
       found = a.K;
       const int room = a.K - count_at_least(key, lo + 1u);
-      int ties = 0;
+      int ties = 0, at_pick = 0;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         const uint64_t eq = __ballot(key[j] == lo);
-        const bool in = key[j] > lo || (key[j] == lo && ties + lanes_before(eq) < room);
-        const uint64_t b = __ballot(in);
-        if (in) picks[at_pick + lanes_before(b)] = pick_of(key[j], j * kLanes + lane);
+        const bool take = key[j] > lo || (key[j] == lo && lanes_before(eq, ties) < room);
+        const uint64_t b = __ballot(take);
+        if (take)
+          picks[lanes_before(b, at_pick)] =
+              (uint64_t)__float_as_uint(v[j]) << 32 | (uint32_t)~(j * kLanes + lane);
         at_pick += __popcll(b);
         ties += __popcll(eq);
       }
     }
+    found = __builtin_amdgcn_readfirstlane(found);
     wave_lds_sync();
-    const uint64_t p = picks[min(lane, found - 1)];
+    uint64_t p = picks[lane];  // whatever was there behind the last
+    const float mine_v = __uint_as_float(pick_key(p));
+    p = (uint64_t)order_key(mine_v) << 32 | (uint32_t)p;
+    picks[lane] = lane < found ? p : 0;  // nothing is ranked behind zeros
+    wave_lds_sync();
     int rank = lane < found ? 0 : kLanes;
-    const float v = key_value(pick_key(p));
-#pragma unroll 4
-    for (int k = 0; k < found; ++k) rank += picks[k] > p ? 1 : 0;
+#pragma unroll 1
+    for (int k = 0; k < found; k += 8) {
+      uint64_t other[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) other[i] = picks[k + i];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) rank += other[i] > p ? 1 : 0;
+    }
     bool close = false;  // another pick is hard to tell from this one, which counts
     if (biased) {
-      const float near = 1e-6f * fmaxf(1.0f, fabsf(v));
+      const float near = 1e-6f * fmaxf(1.0f, fabsf(mine_v));
       int n = 0;
 #pragma unroll 4
       for (int k = 0; k < found; ++k)
-        n += fabsf(key_value(pick_key(picks[k])) - v) <= near ? 1 : 0;
+        n += fabsf(key_value(pick_key(picks[k])) - mine_v) <= near ? 1 : 0;
       close = n > 1 && rank < a.K;  // itself is one
     }
     wave_lds_sync();
     int id = pick_id(p);
     float sel;
     if (biased) {
-      uint32_t next = 0;  // the largest key that is not among the picks
+      float next = -INFINITY;  // the largest that is not among the picks
 #pragma unroll
-      for (int j = 0; j < J; ++j) next = max(next, key[j] < lo ? key[j] : 0u);
-      const float border = key_value(lo), left = key_value(wave_max_u32(next));
-      close = close || crowded || border - left <= 1e-6f * fmaxf(1.0f, fabsf(border));
+      for (int j = 0; j < J; ++j) next = fmaxf(next, v[j] < least ? v[j] : -INFINITY);
+      const float border = least, left = key_value(wave_max_u32(order_key(next)));
+      close = close || !plain || border - left <= 1e-6f * fmaxf(1.0f, fabsf(border));
       // A score in 32 bits plus its bias is off by a few units in the last
       // place, below 5e-7 * max(1, |sum|): neighbours nearer than twice that
       // are told apart in 64 bits.
       if (__ballot(close) != 0) {
-        id = select_wide<J, BF16>(a.logits, at, a.bias, a.E, a.K, lane);
+        id = select_wide<J, BF16>(a.logits, at, a.bias, E, a.K, lane);
         rank = lane;
       }
       sel = rank < a.K ? logistic(load_logit<BF16>(a.logits, at + id)) : 0.0f;
     } else {
-      const float x = pick_key(p) == 1u ? NAN : v;
-      sel = rank < a.K ? (a.sigmoid ? logistic(x) : exp_shifted(x, shift)) : 0.0f;
+      sel = rank < a.K ? (sigmoid ? logistic(mine_v) : exp_shifted(mine_v, shift)) : 0.0f;
     }
-    float out;
-    if (a.renorm)
-      out = a.scale * (sel * reciprocal_or_zero(wave_sum(sel)));
-    else
-      out = a.scale * (a.sigmoid ? sel : sel * reciprocal_or_zero(total));
+    // One division for both: by the picks' sum in lane 0, by all scores' in lane 1.
+    float out = a.scale, inv = 0.0f;
+    if (Sums || a.renorm) {
+      const float picked = a.renorm ? wave_sum(sel) : 0.0f;
+      const float q = reciprocal_or_zero(lane == 0 ? picked : total);
+      inv = read_lane(q, 1);
+      out *= a.renorm ? sel * read_lane(q, 0) : sigmoid ? sel : sel * inv;
+    } else {
+      out *= sel;
+    }
     if (rank < a.K) {
-      a.topk[tok * a.K + rank] = id;
-      a.weights[tok * a.K + rank] = out;
+      int32_t* const ids = a.topk + tok * a.K;
+      float* const weights = a.weights + tok * a.K;
+      ids[(uint32_t)rank] = id;
+      weights[(uint32_t)rank] = out;
+      if (a.stats) atomicAdd(&red_c[id], 1);  // whole numbers: any order
     }
-    if (a.stats) {
-      const float inv = reciprocal_or_zero(total);
+    if (Sums) {
 #pragma unroll
       for (int j = 0; j < J; ++j) acc[j] = fmaf(s[j], inv, acc[j]);
-      if (rank < a.K) atomicAdd(&red_c[id], 1);  // whole numbers: any order
     }
   }
   if (!a.stats) return;
+  if (Sums) {
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const int e = j * kLanes + lane;
-    if (e < a.E) red_p[w * a.E + e] = acc[j];
+    for (int j = 0; j < J; ++j) {
+      const int e = j * kLanes + lane;
+      if (e < E) red_p[w * E + e] = acc[j];
+    }
   }
   if (lane == 0) red_n[w] = n_valid;
   __syncthreads();
@@ -406,7 +454,8 @@ __global__ void __launch_bounds__(kMaxWaves* kLanes) __attribute__((amdgpu_waves
   for (int i = 0; i < waves; ++i) n += red_n[i];
   const auto per = [&](int e, float* p, int32_t* c) {
     float sum = 0.0f;
-    for (int i = 0; i < waves; ++i) sum += red_p[i * a.E + e];
+    if (Sums)
+      for (int i = 0; i < waves; ++i) sum += red_p[i * E + e];
     *p = sum;
     *c = red_c[e];
   };
@@ -415,13 +464,17 @@ __global__ void __launch_bounds__(kMaxWaves* kLanes) __attribute__((amdgpu_waves
     return;
   }
   const int64_t row = (int64_t)r * a.nblk + blk;
-  for (int e = threadIdx.x; e < a.E; e += blockDim.x)
-    per(e, &a.part_p[row * a.E + e], &a.part_c[row * a.E + e]);
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    float p;
+    per(e, &p, &a.part_c[row * E + e]);
+    if (Sums) a.part_p[row * E + e] = p;
+  }
   if (threadIdx.x == 0) a.part_n[row] = n;
 }
 
 // Adds the workgroups' sums of a rank: 1024 threads, as many to an expert as
 // there are, each a fixed share of the partial sums.
+template <bool Sums>
 __global__ void __launch_bounds__(1024) k_route_finish(RouteArgs a, int experts) {
   __shared__ float red[1024 / kLanes];
   __shared__ float part_p[1024];
@@ -438,9 +491,9 @@ __global__ void __launch_bounds__(1024) k_route_finish(RouteArgs a, int experts)
   float sum = 0.0f;
   int32_t cnt = 0;
   if (e < a.E) {
-#pragma unroll 4
+#pragma unroll 16
     for (int i = share; i < a.nblk; i += shares) {
-      sum += a.part_p[(row + i) * a.E + e];
+      if (Sums) sum += a.part_p[(row + i) * a.E + e];
       cnt += a.part_c[(row + i) * a.E + e];
     }
   }
@@ -589,10 +642,11 @@ __global__ void __launch_bounds__(256) k_route_grad(RouteGradArgs a, int nblk) {
 
 // How a call is cut: waves per workgroup and workgroups per rank.  Up to 32
 // tokens a rank one workgroup of 16 waves does it all in one launch, at most
-// two tokens a wave of about 3.5 us each; beyond that workgroups of eight
-// waves, four to a compute unit (1024 in all), and a second launch of about
-// 6 us adds their partial sums.  Without counts, sums or loss there is nothing
-// to add and every four tokens get a workgroup.
+// two tokens a wave; beyond that workgroups of eight waves, four to a compute
+// unit (1024 in all), and a second launch of 5 to 7 us adds their partial sums
+// (R=8, E=256 with a bias: 32 tokens 9.2 us in one launch and 10.3 in two, 48
+// tokens 11.0 and 10.4, 64 tokens 13.6 and 10.3).  Without counts, sums or loss
+// there is nothing to add and every four tokens get a workgroup.
 constexpr int kOneLaunchTokens = 32;
 
 void route_cut(int R, int S, bool stats, int* waves, int* nblk) {
@@ -612,14 +666,41 @@ size_t route_workspace(int R, int S, int E, bool stats) {
   return nblk == 1 || !stats ? 0 : (size_t)R * nblk * (2 * (size_t)E + 1) * 4;
 }
 
+template <int J, bool BF16, int Score, bool Sums>
+void launch_route(const RouteArgs& a, int waves, hipStream_t s) {
+  const size_t words = (size_t)waves * kLanes * 2 + (a.stats ? (size_t)a.E + 2 * waves : 0) +
+                       (Sums && a.stats ? (size_t)waves * a.E : 0);
+  const dim3 grid(a.nblk, a.R), block(waves * kLanes);
+  if (a.E == J * kLanes)
+    hipLaunchKernelGGL((k_route<J, BF16, Score, Sums, true>), grid, block, words * 4, s, a);
+  else
+    hipLaunchKernelGGL((k_route<J, BF16, Score, Sums, false>), grid, block, words * 4, s, a);
+}
+
+template <int J, bool BF16, int Score>
+void launch_route(const RouteArgs& a, int waves, hipStream_t s) {
+  // softmax weights that are not renormalised need the sum of all scores
+  if (a.sums || (Score == kSoftmax && !a.renorm))
+    launch_route<J, BF16, Score, true>(a, waves, s);
+  else
+    launch_route<J, BF16, Score, false>(a, waves, s);
+}
+
 template <int J, bool BF16>
 hipError_t run_route(const RouteArgs& a, int waves, hipStream_t s) {
-  const size_t lds = ((size_t)waves * kLanes * 2 + (a.stats ? (size_t)waves * a.E + a.E + 2 * waves : 0)) * 4;
-  hipLaunchKernelGGL((k_route<J, BF16>), dim3(a.nblk, a.R), dim3(waves * kLanes), lds, s, a);
+  if (!a.sigmoid)
+    launch_route<J, BF16, kSoftmax>(a, waves, s);
+  else if (a.bias == nullptr)
+    launch_route<J, BF16, kSigmoid>(a, waves, s);
+  else
+    launch_route<J, BF16, kBiased>(a, waves, s);
   if (a.stats && a.nblk > 1) {
     int experts = kLanes;  // the power of two that holds E
     while (experts < a.E) experts *= 2;
-    hipLaunchKernelGGL(k_route_finish, dim3(a.R), dim3(1024), 0, s, a, experts);
+    if (a.sums)
+      hipLaunchKernelGGL(k_route_finish<true>, dim3(a.R), dim3(1024), 0, s, a, experts);
+    else
+      hipLaunchKernelGGL(k_route_finish<false>, dim3(a.R), dim3(1024), 0, s, a, experts);
   }
   return hipGetLastError();
 }
@@ -698,6 +779,7 @@ moon_status moon_route(const moon_route_config* cfg, const void* logits_rse, con
   a.coef = cfg->loss_coef;
   a.stats = tokens_per_expert_re != nullptr || valid_tokens_r != nullptr ||
             prob_sums_re != nullptr || loss_r != nullptr;
+  a.sums = prob_sums_re != nullptr || loss_r != nullptr;
   int waves;
   moon::route_cut(a.R, a.S, a.stats != 0, &waves, &a.nblk);
   const size_t need = moon::route_workspace(a.R, a.S, a.E, a.stats != 0);

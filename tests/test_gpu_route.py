@@ -329,3 +329,51 @@ def test_route_refusals(env):
         moon.moon_route_backward(x, topk, torch.zeros_like(x), d_loss=torch.zeros(2, device=dev))
     with pytest.raises(ValueError):
         moon.moon_route_backward(x, topk, torch.zeros((2, 4, 8), dtype=torch.bfloat16, device=dev))
+
+
+@pytest.mark.parametrize("E,K", [(70, 8), (128, 4), (384, 8), (384, 48), (512, 64)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid", "biased"])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_route_nan_among_numbers(env, E, K, score, bf16):
+    """NaN logits, quiet and signalling, of both signs: next to a lane's largest
+    number, in rows with fewer than K numbers and in rows without one.  They
+    rank behind -inf, and weights over numbers alone are not touched by them
+    (relative error as above: the sum's terms, twice the exponent's span, 64)."""
+    moon, torch, dev = env
+    say(f"[case] NaN E={E} K={K} {score} bf16={bf16}")
+    rng = np.random.default_rng(E + K)
+    S = 60
+    bits = (3.0 * rng.standard_normal((1, S, E))).astype(np.float32).view(np.uint32) & 0xFFFF0000
+    nans = np.array([0x7F810000, 0xFF810000, 0x7FC00000, 0xFFC10000], np.uint32)
+    part = np.linspace(0.0, 1.0, S)[None, :, None]  # the share of NaN grows by token
+    bits = np.where(rng.random(bits.shape) < part, rng.choice(nans, bits.shape), bits)
+    bits = np.where(rng.random(bits.shape) < 0.1, np.uint32(0xFF800000), bits)
+    bits[0, -1] = nans[0]
+    bits[0, 0, :] = np.where(np.arange(E) < E // 2, np.uint32(0x42F00000), nans[1])  # 120.0
+    x = bits.astype(np.uint32).view(np.float32)
+    lg = torch.from_numpy(x.copy()).to(dev) if not bf16 else \
+        torch.from_numpy((bits >> 16).astype(np.uint16).view(np.int16)).to(dev).view(torch.bfloat16)
+    bias = (rng.integers(-8, 9, E) / 4.0).astype(np.float32) if score == "biased" else None
+    topk = torch.empty((1, S, K), dtype=torch.int32, device=dev)
+    w = torch.empty((1, S, K), device=dev)
+    moon.moon_route(lg, topk, w, moon.MOON_ROUTE_RENORM | (moon.MOON_ROUTE_SIGMOID if score != "softmax" else 0),
+                    bias=None if bias is None else torch.from_numpy(bias).to(dev))
+    torch.cuda.synchronize()
+    topk, w = topk.cpu().numpy()[0], w.double().cpu().numpy()[0]
+    for t in range(S):
+        with np.errstate(invalid="ignore"):
+            z = x[0, t].astype(np.float64)
+        num = ~np.isnan(z)
+        top = z[num & ~np.isneginf(z)].max(initial=-np.inf)
+        with np.errstate(over="ignore", invalid="ignore"):
+            s = 1.0 / (1.0 + np.exp(-z)) if score != "softmax" else \
+                np.exp(z - (top if np.isfinite(top) else 0.0))
+        key = z if bias is None else np.where(np.isneginf(z), -np.inf, s + bias)
+        ids = np.lexsort((np.arange(E), -np.where(num, key, 0.0), ~num))[:K]
+        assert (topk[t] == ids).all(), t
+        if num[ids].all():
+            den = s[ids].sum()
+            want = s[ids] / (den if den > 0 else 1.0)
+            assert (np.abs(w[t] - want) <= (E + 2 * 130 + 64) * EPS * want + 1e-37).all(), t
+        else:
+            assert np.isnan(w[t]).all(), t
