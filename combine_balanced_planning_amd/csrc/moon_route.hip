@@ -209,27 +209,51 @@ __device__ __forceinline__ void finish_rank(const RouteArgs& a, int r, int n, fl
   }
 }
 
+// The kernel's arguments, read again: what only the end of k_route needs would
+// else sit in scalar registers through its loop and push others out (36
+// spilled against 15, 77 against 73 us a call at the size below).
+__device__ __forceinline__ RouteArgs late_args() {
+  const __attribute__((address_space(4))) RouteArgs* p =
+      (const __attribute__((address_space(4))) RouteArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  RouteArgs a;
+  a.counts = p->counts;
+  a.tokens = p->tokens;
+  a.psum = p->psum;
+  a.loss = p->loss;
+  a.part_p = p->part_p;
+  a.part_c = p->part_c;
+  a.part_n = p->part_n;
+  a.S = p->S;
+  a.E = p->E;
+  a.K = p->K;
+  a.nblk = p->nblk;
+  a.coef = p->coef;
+  return a;
+}
+
 // Held to 64 registers for eight waves a SIMD: a token is a chain of dependent
 // steps, and more waves hide it (an earlier version took 113 us with fewer and
 // 96 with eight).  What selects, whether sums over tokens (or a token's sum of
 // scores) are wanted and whether the words are full are template arguments:
-// told at run time they cost branches and spilled scalars, 96 against 73 us a
-// call at R=16, S=8192, E=384, fp32.  There a token takes 233 vector and 184
-// scalar instructions, the kernel 67 us with the vector unit busy 70 % of
-// them; the logits alone take 41 us to read.
+// told at run time they cost branches and spilled scalars, 96 against 77 us a
+// call at R=16, S=8192, E=384, fp32 (67 now).  There the kernel takes 63 us, the
+// vector unit busy 72 % of them; the logits alone take 41 us to read.
 template <int J, bool BF16, int Score, bool Sums, bool Whole>
 __global__ void __launch_bounds__(kMaxWaves* kLanes) __attribute__((amdgpu_waves_per_eu(8)))
     k_route(RouteArgs a) {
   constexpr bool biased = Score == kBiased, sigmoid = Score != kSoftmax;
   const int E = Whole ? J * kLanes : a.E;  // Whole: the words are full
-  extern __shared__ float lds[];  // [waves][64] picks; with stats also [E] counts,
-                                  // [waves] tokens, [waves]; with Sums [waves][E] sums
+  extern __shared__ float lds[];  // [waves][64] picks; biased: [waves][64] their scores;
+                                  // with stats also [E] counts, [waves] tokens,
+                                  // [waves]; with Sums [waves][E] sums
   const int lane = threadIdx.x & (kLanes - 1);
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
   const int waves = blockDim.x / kLanes;
   const int r = blockIdx.y, blk = blockIdx.x;
   uint64_t* const picks = reinterpret_cast<uint64_t*>(lds) + w * kLanes;
-  int32_t* const red_c = reinterpret_cast<int32_t*>(lds + 2 * waves * kLanes);
+  float* const scores = lds + 2 * waves * kLanes + w * kLanes;
+  int32_t* const red_c = reinterpret_cast<int32_t*>(lds + (biased ? 3 : 2) * waves * kLanes);
   int32_t* const red_n = red_c + E;
   float* const red_l = reinterpret_cast<float*>(red_n + waves);
   float* const red_p = red_l + waves;
@@ -312,18 +336,15 @@ __global__ void __launch_bounds__(kMaxWaves* kLanes) __attribute__((amdgpu_waves
       }
       total = wave_sum(total);
     }
-    // A few maxima too many cost less than the rounds that would tell them,
-    // unless every pair is looked at twice.
-    const int enough = biased ? a.K : a.K + (a.K >> 1);
+    // A few maxima too many cost less than the rounds that would tell them.
+    const int enough = a.K + (a.K >> 1);
     while (hi - lo > 1u) {
       const uint32_t mid = lo + (hi - lo) / 2;
       const int n = __popcll(__ballot(mine >= mid));
-      if (n < a.K) {
-        hi = mid;
-        continue;
-      }
-      lo = mid;
-      if (n <= enough) break;
+      const bool many = n >= a.K;
+      lo = many ? mid : lo;
+      // (hi = lo ends it)
+      hi = many ? (n <= enough ? mid : hi) : mid;
     }
     // Comparisons of numbers from here: NaN takes no part, so a row that needs
     // one finds fewer than K.
@@ -339,10 +360,13 @@ __global__ void __launch_bounds__(kMaxWaves* kLanes) __attribute__((amdgpu_waves
     const bool plain = found >= a.K && found <= kLanes;
     if (plain) {
 #pragma unroll
-      for (int j = 0; j < J; ++j)
-        if (v[j] >= least)
-          picks[lanes_before(in[j], first[j])] =
-              (uint64_t)__float_as_uint(v[j]) << 32 | (uint32_t)~(j * kLanes + lane);
+      for (int j = 0; j < J; ++j) {
+        if (v[j] >= least) {
+          const int i = lanes_before(in[j], first[j]);
+          picks[i] = (uint64_t)__float_as_uint(v[j]) << 32 | (uint32_t)~(j * kLanes + lane);
+          if (biased) scores[i] = s[j];
+        }
+      }
     } else {
       // Too many for the lanes (large K, long runs of equal keys) or NaN: on by
       // all keys, and of those equal at the end the first ones, as many as
@@ -382,39 +406,42 @@ __global__ void __launch_bounds__(kMaxWaves* kLanes) __attribute__((amdgpu_waves
     wave_lds_sync();
     int rank = lane < found ? 0 : kLanes;
 #pragma unroll 1
-    for (int k = 0; k < found; k += 8) {
-      uint64_t other[8];
+    for (int k = 0; k < found; k += 4) {
+      uint64_t other[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) other[i] = picks[k + i];
+      for (int i = 0; i < 4; ++i) other[i] = picks[k + i];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) rank += other[i] > p ? 1 : 0;
-    }
-    bool close = false;  // another pick is hard to tell from this one, which counts
-    if (biased) {
-      const float near = 1e-6f * fmaxf(1.0f, fabsf(mine_v));
-      int n = 0;
-#pragma unroll 4
-      for (int k = 0; k < found; ++k)
-        n += fabsf(key_value(pick_key(picks[k])) - mine_v) <= near ? 1 : 0;
-      close = n > 1 && rank < a.K;  // itself is one
+      for (int i = 0; i < 4; ++i) rank += other[i] > p ? 1 : 0;
     }
     wave_lds_sync();
     int id = pick_id(p);
     float sel;
     if (biased) {
-      float next = -INFINITY;  // the largest that is not among the picks
-#pragma unroll
-      for (int j = 0; j < J; ++j) next = fmaxf(next, v[j] < least ? v[j] : -INFINITY);
-      const float border = least, left = key_value(wave_max_u32(order_key(next)));
-      close = close || !plain || border - left <= 1e-6f * fmaxf(1.0f, fabsf(border));
       // A score in 32 bits plus its bias is off by a few units in the last
       // place, below 5e-7 * max(1, |sum|): neighbours nearer than twice that
-      // are told apart in 64 bits.
+      // are told apart in 64 bits.  Only pairs of neighbours need a look, and
+      // the largest that was not picked only if nothing between is picked.
+      const float near = 1e-6f * fmaxf(1.0f, fabsf(mine_v));
+      float* const by_rank = reinterpret_cast<float*>(picks);
+      if (rank < found) by_rank[rank] = mine_v;
+      wave_lds_sync();
+      const float below = by_rank[min(rank, found - 2) + 1];
+      sel = scores[lane];
+      wave_lds_sync();
+      bool close = !plain || (rank < a.K && rank + 1 < found && mine_v - below <= near);
+      if (found == a.K) {
+        float next = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < J; ++j) next = fmaxf(next, v[j] < least ? v[j] : -INFINITY);
+        const float left = key_value(wave_max_u32(order_key(next)));
+        close = close || least - left <= 1e-6f * fmaxf(1.0f, fabsf(least));
+      }
       if (__ballot(close) != 0) {
         id = select_wide<J, BF16>(a.logits, at, a.bias, E, a.K, lane);
         rank = lane;
+        sel = lane < a.K ? logistic(load_logit<BF16>(a.logits, at + id)) : 0.0f;
       }
-      sel = rank < a.K ? logistic(load_logit<BF16>(a.logits, at + id)) : 0.0f;
+      if (rank >= a.K) sel = 0.0f;
     } else {
       sel = rank < a.K ? (sigmoid ? logistic(mine_v) : exp_shifted(mine_v, shift)) : 0.0f;
     }
@@ -441,6 +468,7 @@ __global__ void __launch_bounds__(kMaxWaves* kLanes) __attribute__((amdgpu_waves
     }
   }
   if (!a.stats) return;
+  const RouteArgs late = late_args();
   if (Sums) {
 #pragma unroll
     for (int j = 0; j < J; ++j) {
@@ -459,17 +487,17 @@ __global__ void __launch_bounds__(kMaxWaves* kLanes) __attribute__((amdgpu_waves
     *p = sum;
     *c = red_c[e];
   };
-  if (a.nblk == 1) {
-    finish_rank(a, r, n, red_l, per);
+  if (late.nblk == 1) {
+    finish_rank(late, r, n, red_l, per);
     return;
   }
-  const int64_t row = (int64_t)r * a.nblk + blk;
+  const int64_t row = (int64_t)r * late.nblk + blk;
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
     float p;
-    per(e, &p, &a.part_c[row * E + e]);
-    if (Sums) a.part_p[row * E + e] = p;
+    per(e, &p, &late.part_c[row * E + e]);
+    if (Sums) late.part_p[row * E + e] = p;
   }
-  if (threadIdx.x == 0) a.part_n[row] = n;
+  if (threadIdx.x == 0) late.part_n[row] = n;
 }
 
 // Adds the workgroups' sums of a rank: 1024 threads, as many to an expert as
@@ -668,7 +696,7 @@ size_t route_workspace(int R, int S, int E, bool stats) {
 
 template <int J, bool BF16, int Score, bool Sums>
 void launch_route(const RouteArgs& a, int waves, hipStream_t s) {
-  const size_t words = (size_t)waves * kLanes * 2 + (a.stats ? (size_t)a.E + 2 * waves : 0) +
+  const size_t words = (size_t)waves * kLanes * (Score == kBiased ? 3 : 2) + (a.stats ? (size_t)a.E + 2 * waves : 0) +
                        (Sums && a.stats ? (size_t)waves * a.E : 0);
   const dim3 grid(a.nblk, a.R), block(waves * kLanes);
   if (a.E == J * kLanes)
