@@ -270,10 +270,10 @@ __global__ void __launch_bounds__(kMaxWaves* kLanes) __attribute__((amdgpu_waves
   }
   int32_t n_valid = 0;
   // The next token's logits are on their way while one is worked on.
-  const int step = a.nblk * waves;
+  const uint32_t step = a.nblk * waves, tokens = a.S;  // a sum of the two fits
   float ahead[J];
   uint32_t ahead_ok = 1;
-  const auto fetch = [&](int t) {
+  const auto fetch = [&](uint32_t t) {
     const int64_t tok = (int64_t)r * a.S + t;
     if (a.valid != nullptr) ahead_ok = a.valid[tok];
     const void* const row = static_cast<const char*>(a.logits) + tok * E * (BF16 ? 2 : 4);
@@ -283,8 +283,9 @@ __global__ void __launch_bounds__(kMaxWaves* kLanes) __attribute__((amdgpu_waves
       ahead[j] = load_logit<BF16>(row, Whole ? e : min(e, (uint32_t)E - 1));
     }
   };
-  if (blk * waves + w < a.S) fetch(blk * waves + w);
-  for (int t = blk * waves + w; t < a.S; t += step) {
+  const uint32_t begin = blk * waves + w;
+  if (begin < tokens) fetch(begin);
+  for (uint32_t t = begin; t < tokens; t += step) {
     const int64_t tok = (int64_t)r * a.S + t;
     const int64_t at = tok * E;
     const int ok = __builtin_amdgcn_readfirstlane((int)ahead_ok);
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(kMaxWaves* kLanes) __attribute__((amdgpu_waves
       s[j] = ahead[j];
       v[j] = j * kLanes + lane < E ? s[j] : NAN;
     }
-    if (t + step < a.S) fetch(t + step);
+    if (t + step < tokens) fetch(t + step);
     if (ok == 0) {
       if (lane < a.K) {
         a.topk[tok * a.K + lane] = 0;
@@ -561,11 +562,11 @@ __global__ void __launch_bounds__(256) k_route_grad(RouteGradArgs a, int nblk) {
   }
   // The next token's logits, ids and weight gradients are on their way while
   // one is worked on.
-  const int step = nblk * 4;
+  const uint32_t step = nblk * 4, tokens = a.S;  // a sum of the two fits
   float ahead[J], ahead_dw = 0.0f;
   int32_t ahead_id = -1;
   uint32_t ahead_ok = 1;
-  const auto fetch = [&](int t) {
+  const auto fetch = [&](uint32_t t) {
     const int64_t tok = (int64_t)r * a.S + t;
     if (a.valid != nullptr) ahead_ok = a.valid[tok];
 #pragma unroll
@@ -576,8 +577,9 @@ __global__ void __launch_bounds__(256) k_route_grad(RouteGradArgs a, int nblk) {
       ahead_dw = a.d_weights[tok * a.K + lane];
     }
   };
-  if ((int)blockIdx.x * 4 + w < a.S) fetch(blockIdx.x * 4 + w);
-  for (int t = blockIdx.x * 4 + w; t < a.S; t += step) {
+  const uint32_t begin = blockIdx.x * 4 + w;
+  if (begin < tokens) fetch(begin);
+  for (uint32_t t = begin; t < tokens; t += step) {
     const int64_t at = ((int64_t)r * a.S + t) * a.E;
     const int ok = __builtin_amdgcn_readfirstlane((int)ahead_ok);
     float d[J], x[J];
@@ -586,7 +588,7 @@ __global__ void __launch_bounds__(256) k_route_grad(RouteGradArgs a, int nblk) {
     const int id = ahead_id;
     const bool picked = id >= 0 && id < a.E;
     const float dw = picked ? ahead_dw : 0.0f;
-    if (t + step < a.S) fetch(t + step);
+    if (t + step < tokens) fetch(t + step);
     if (ok == 0) {
 #pragma unroll
       for (int j = 0; j < J; ++j) d[j] = 0.0f;
@@ -684,7 +686,7 @@ void route_cut(int R, int S, bool stats, int* waves, int* nblk) {
     return;
   }
   *waves = stats ? 8 : 4;
-  const int want = (S + *waves - 1) / *waves;
+  const int want = (int)(((int64_t)S + *waves - 1) / *waves);
   *nblk = std::min(want, stats ? std::max(2, 1024 / R) : 65536);
 }
 
@@ -735,7 +737,7 @@ hipError_t run_route(const RouteArgs& a, int waves, hipStream_t s) {
 
 template <int J, bool BF16>
 hipError_t run_route_grad(const RouteGradArgs& a, hipStream_t s) {
-  const int nblk = std::max(1, std::min((a.S + 3) / 4, 4096 / a.R));
+  const int nblk = std::max(1, std::min((int)(((int64_t)a.S + 3) / 4), 4096 / a.R));
   hipLaunchKernelGGL((k_route_grad<J, BF16>), dim3(nblk, a.R), dim3(256), 0, s, a, nblk);
   return hipGetLastError();
 }

@@ -377,3 +377,25 @@ def test_route_nan_among_numbers(env, E, K, score, bf16):
             assert (np.abs(w[t] - want) <= (E + 2 * 130 + 64) * EPS * want + 1e-37).all(), t
         else:
             assert np.isnan(w[t]).all(), t
+
+
+def test_route_most_tokens(env):
+    """2^31 - 1 tokens, the most there can be: token counters and the cut into
+    workgroups stay in range (20 GB; one expert, so ids 0 and weights 1.5)."""
+    moon, torch, dev = env
+    say("[case] 2^31 - 1 tokens")
+    S = 2 ** 31 - 1
+    x = torch.zeros((1, S, 1), dtype=torch.bfloat16, device=dev)
+    topk = torch.full((1, S, 1), -1, dtype=torch.int32, device=dev)
+    w = torch.zeros((1, S, 1), device=dev)
+    moon.moon_route(x, topk, w, 0, 1.5)
+    torch.cuda.synchronize()
+    for a in range(0, S, 2 ** 28):  # in parts that torch indexes with 32 bits
+        assert int(topk[0, a:a + 2 ** 28].abs().max()) == 0
+        assert float(w[0, a:a + 2 ** 28].min()) == 1.5 == float(w[0, a:a + 2 ** 28].max())
+    x.fill_(1.0)
+    d = torch.ones_like(x)
+    moon.moon_route_backward(x, topk, d, 0, 1.5, d_weights=w)
+    torch.cuda.synchronize()
+    for a in range(0, S, 2 ** 28):  # a softmax over one expert has no gradient
+        assert float(d[0, a:a + 2 ** 28].float().abs().max()) == 0.0
