@@ -403,7 +403,8 @@ __global__ void __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_
       const int e = tid * each + i;
       if (e >= entries) break;
       const Span s = group_span(g, e / g.per, e % g.per);
-      const int t = (s.real_end - s.begin + kTile - 1) / kTile;
+      // (padding without a route still has a tile, which clears it)
+      const int t = max((s.real_end - s.begin + kTile - 1) / kTile, s.end > s.begin ? 1 : 0);
       first[e + 1] = t;
       sum += t;
     }
@@ -488,7 +489,7 @@ __global__ void __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_
       const int tid = fresh_thread_id(), f = (tid >> 4) & 15, r = tid & 15;
       src_scale = is_w ? ((f >> 2) & 1 ? ws[1] : ws[0]) +
                              (int64_t)(t.n0 + min(weight_row(f >> 1, (f & 1) * 16 + r), nr - 1)) * blocks
-                       : a.xs + (base + min(tid - kTile, mr - 1)) * blocks;
+                       : a.xs + (base + max(min(tid - kTile, mr - 1), 0)) * blocks;
     }
   };
 

@@ -270,3 +270,20 @@ def test_refusals(env):
     n12 = tuple(t[..., :12, :].contiguous() for t in w)  # 12 outputs: no multiple of 8
     with pytest.raises(moon.MoonError):
         moon.moon_expert_gemm_mx4(**{**ok, "weight": n12, "y": y[:, :12].contiguous()})
+
+
+@pytest.mark.parametrize("rows", [3, 20, 300])
+@pytest.mark.parametrize("K", [512, 544])
+def test_padding_without_routes(env, rows, K):
+    """Groups of nothing but padding, which only a caller's own arrays have: the
+    first, one between others and the last, in every kernel."""
+    say(f"[case] groups of padding only, rows={rows} K={K}")
+    c = Case(env, own(2, 8, 1, [rows] * 8, [[rows], [rows]]), 8, 4, K, 72, seed=rows)
+    cu, zfr = c.arrays["cu_seqlens"], c.arrays["zero_fill_ranges"]
+    for u, g in [(0, 0), (0, 2), (1, 5), (1, 8)]:
+        zfr[u, g, 0] = cu[u, g - 1] if g > 0 else 0
+    c.kind = ref.row_kinds(c.arrays, c.NvS)
+    assert (c.kind == 2).sum() >= 4 * rows
+    c.xs[c.kind != 1], c.row_w[c.kind != 1] = 255, np.nan
+    c.plan = {k: c.put(v) for k, v in c.arrays.items()}
+    c.check(env)
