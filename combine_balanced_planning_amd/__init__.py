@@ -385,7 +385,8 @@ def _groups(plan, rows, dev):
     else:
         cu, etc, dst = plan["cu_seqlens"], plan["experts_to_copy"], plan.get("dst")
         cs, es = cu.shape, etc.shape
-        if len(cs) != 2 or len(es) != 2 or es[0] != cs[0] or cs[1] <= es[1] or es[1] < 1:
+        if len(cs) != 2 or len(es) != 2 or es[0] != cs[0] or cs[0] < 1 or cs[1] <= es[1] or \
+                es[1] < 1:
             raise ValueError("cu_seqlens must be [R, E+B] and experts_to_copy [R, B]")
         R, EB = cs
         pa = moon_plan_arrays()

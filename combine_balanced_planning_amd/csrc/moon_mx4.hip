@@ -31,7 +31,7 @@ struct Mx4Args {
   int64_t rows;
   int32_t cols;
   int32_t rank_rows;  // rows per rank window (with a plan)
-  int32_t per_wg;     // rows per workgroup, at most 64
+  int32_t per_wg;     // rows per workgroup, with a plan at most 64
   int32_t lanes;      // lanes per row, a power of two
   int32_t words;      // scale bytes are stored four at a time
 };
@@ -226,6 +226,8 @@ moon_status launch(Mx4Args a, int32_t dtype, const moon_plan_arrays* plan, hipSt
   // are one word) for long thin arrays.
   a.per_wg = (int)std::max<int64_t>(1, std::min<int64_t>(64, a.rows / 16384));
   a.per_wg = std::max(a.per_wg, std::min(64, 256 / a.lanes));
+  // A launch has fewer than 2^32 threads: from 2^30 rows on more rows each.
+  if (plan == nullptr) a.per_wg = std::max(a.per_wg, (int)(a.rows >> 23) + 1);
   const bool bf = dtype == MOON_DTYPE_BF16;
   if (plan != nullptr) {
     const dim3 grid((g.NvS + a.per_wg - 1) / a.per_wg, g.R);

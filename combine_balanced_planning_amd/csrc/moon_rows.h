@@ -161,7 +161,7 @@ inline moon_status make_groups(const moon_plan_arrays* p, Groups* g) {
     return MOON_ERR_INVALID_ARG;
   if (p->R < 1 || p->E < 1 || p->B < 1 || p->NvS < 1) return MOON_ERR_INVALID_ARG;
   if (p->E % p->R != 0) return MOON_ERR_TOPOLOGY;
-  if (p->R > 32 || p->E > 512 || (int64_t)p->R * p->B > 8192 ||
+  if (p->R > 32 || p->E > 512 || (int64_t)p->R * p->B > 8192 || p->NvS > 1 << 29 ||
       (int64_t)p->R * p->NvS >= (int64_t)1 << 31)
     return MOON_ERR_UNSUPPORTED;
   g->cu = p->cu_seqlens;

@@ -278,7 +278,8 @@ moon_status moon_reduce_grad(moon_ctx* ctx, const moon_comm_plan* plan,
  * Those that walk the window rows take the plan's arrays (moon_plan_view, or
  * the caller's own of moon_plan_noalloc) and read cu_seqlens, zero_fill_ranges,
  * status, R, E, B, NvS and N of them; the other fields may be null, and N, by
- * which a kernel is chosen, 0.  The arrays
+ * which a kernel is chosen, 0.  NvS is at most
+ * 2^29.  The arrays
  * are laid out as the planner does: rank u's rows belong to its own experts
  * u*E/R ... and to its slots.  A plan whose device status is not OK
  * writes nothing.  Rows that hold routes are computed, padding rows of the

@@ -231,3 +231,25 @@ def test_refusals(env):
     plan["zero_fill_ranges"] = plan["zero_fill_ranges"][:, :1].contiguous()
     with pytest.raises(ValueError):
         moon.moon_mx4_quantize(x, u8(4, 32), u8(4, 2), plan=plan)
+
+
+def test_rows_of_more_than_one_launch_could_cover(env):
+    """2^30 + 5 rows of 32 values (64 + 16 GiB): with 64 rows a workgroup they
+    would take more threads than a launch may have."""
+    moon, torch, dev = env
+    n = 2 ** 30 + 5
+    say(f"[case] {n} rows")
+    if torch.cuda.mem_get_info(dev)[0] < 90 * 2 ** 30:
+        pytest.skip("needs 90 GiB")
+    x = torch.full((n, 32), 1.5, dtype=torch.bfloat16, device=dev)
+    x[-1] = -3.0
+    q = torch.zeros((n, 16), dtype=torch.uint8, device=dev)
+    s = torch.zeros((n, 1), dtype=torch.uint8, device=dev)
+    moon.moon_mx4_quantize(x, q, s)
+    del x
+    torch.cuda.synchronize()
+    words = q.view(torch.int64)  # 1.5 = 6 * 2^-2, -3 = -6 * 2^-1
+    for a in range(0, n - 1, 2 ** 27):
+        b = min(a + 2 ** 27, n - 1)
+        assert bool((words[a:b] == 0x7777777777777777).all()) and bool((s[a:b] == 125).all())
+    assert q[-1].tolist() == [0xFF] * 16 and s[-1].item() == 126

@@ -135,3 +135,23 @@ def test_swiglu8_refusals(moon):
         for kw, want in BAD_PLANS:
             assert f(plan=arrays(moon, **kw)) == want, kw
     assert grad(dw=ODD) == inv
+
+
+def test_windows_beyond_a_launch_are_refused(moon):
+    """2^29 rows a window are the most that a launch is sure to cover."""
+    n = (1 << 29) + 1
+    for R, status in ((1, moon.MOON_ERR_UNSUPPORTED), (2, moon.MOON_ERR_UNSUPPORTED)):
+        assert moon._lib.moon_mx4_quantize(PTR, 1, R * n, 32, arrays(moon, R=R, NvS=n), PTR, PTR,
+                                           None) == status
+        assert moon._lib.moon_swiglu_save8(arrays(moon, R=R, NvS=n), PTR, None, 32, PTR, PTR, PTR,
+                                           None) == status
+
+
+def test_plan_arrays_of_no_rank_are_refused(moon):
+    """A plan dict of empty arrays is an error of its arguments."""
+    import torch
+    i32 = dict(dtype=torch.int32)
+    plan = {"cu_seqlens": torch.empty((0, 4), **i32), "experts_to_copy": torch.empty((0, 1), **i32),
+            "zero_fill_ranges": torch.empty((0, 4, 2), **i32), "status": torch.empty((1,), **i32)}
+    with pytest.raises(ValueError, match="cu_seqlens"):
+        moon._groups(plan, 0, 0)
