@@ -751,7 +751,11 @@ moon_status launch(const ExpertArgs& a, const Groups& g, hipStream_t s) {
     if (hipGetDevice(&dev) == hipSuccess)
       (void)hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
     const int wgs = std::max(8, cus / 8 * 8);
-    if (a.K % 512 == 0)
+    // whole turns of scales go straight into LDS, from whole 16 bytes
+    bool whole = a.K % 512 == 0 && is_aligned(a.xs, 16);
+    for (int p = 0; p < (Swiglu ? 2 : 1); ++p)
+      whole = whole && is_aligned(a.w[p].es, 16) && is_aligned(a.w[p].ss, 16);
+    if (whole)
       hipLaunchKernelGGL((k_expert_tiles<Swiglu, true>), dim3(wgs), dim3(kTileThreads), 0, s, a, g);
     else
       hipLaunchKernelGGL((k_expert_tiles<Swiglu, false>), dim3(wgs), dim3(kTileThreads), 0, s, a, g);

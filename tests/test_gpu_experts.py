@@ -287,3 +287,26 @@ def test_padding_without_routes(env, rows, K):
     c.xs[c.kind != 1], c.row_w[c.kind != 1] = 255, np.nan
     c.plan = {k: c.put(v) for k, v in c.arrays.items()}
     c.check(env)
+
+
+@pytest.mark.parametrize("rows", [3, 20, 300])
+@pytest.mark.parametrize("off", [1, 4])
+def test_scales_anywhere(env, rows, off):
+    """Scale bytes may start at any address, whole turns of them too."""
+    moon, torch, dev = env
+    say(f"[case] scales {off} bytes off, rows={rows}")
+    c = Case(env, own(1, 4, 1, [rows] * 4, [[rows]]), 4, 1, 512, 72, seed=rows + off)
+
+    def moved(a):
+        buf = torch.full((a.size + 16,), 255, dtype=torch.uint8, device=dev)
+        buf[off:off + a.size] = c.put(a).view(-1)
+        return buf[off:off + a.size].view(a.shape)
+
+    G, bound = c.products(c.ws[0])
+    eq, es, sq, ss = c.ws[0]
+    for xs, w in ((moved(c.xs), c.dev(c.ws[0])), (c.put(c.xs), (c.put(eq), moved(es), c.put(sq), c.put(ss))),
+                  (c.put(c.xs), (c.put(eq), c.put(es), c.put(sq), moved(ss)))):
+        y = torch.full((c.NvS, 72), 77.0, dtype=torch.bfloat16, device=dev)
+        moon.moon_expert_gemm_mx4(c.plan, c.put(c.xq), xs, w, y)
+        torch.cuda.synchronize()
+        c.check_rows(y.double().cpu().numpy(), G, 512 * 2.0 ** -23 * bound)
