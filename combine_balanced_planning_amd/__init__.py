@@ -358,15 +358,18 @@ def _dtype_code(t, name):
     return _DTYPES[t.dtype]
 
 
-# The raw handle of a device's current stream without building a Stream object.
+# The raw handle of a device's current stream without building a Stream object,
+# and the current device without the check for a first use (a call has tensors
+# on a device).  Small calls are bound by the host: 8 us, 3 of them the launch.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _call(dev, fn, *args, stream=None):
     """Calls the library with `dev` current (switching to it and back if it is not)."""
     s = _raw_stream(dev) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         st = fn(*args, s)
     else:
         with torch.cuda.device(dev):
@@ -401,11 +404,17 @@ def _groups(plan, rows, dev):
     return pa
 
 
-def _route_config(logits, K, flags, scale, loss_coef):
-    if logits.dim() != 3:
-        raise ValueError(f"logits must be [R, S, E], got {tuple(logits.shape)}")
-    R, S, E = logits.shape
-    return moon_route_config(R, S, E, K, _dtype_code(logits, "logits"), flags, scale, loss_coef)
+def _route_config(logits, topk, flags, scale, loss_coef):
+    """(moon_route_config, R, S, E, K) of logits [R, S, E] and topk [R, S, K]."""
+    ls, ts = logits.shape, topk.shape
+    if len(ls) != 3:
+        raise ValueError(f"logits must be [R, S, E], got {tuple(ls)}")
+    R, S, E = ls
+    if len(ts) != 3 or ts[0] != R or ts[1] != S:
+        raise ValueError(f"topk must be [R, S, K], got {tuple(ts)}")
+    K = ts[2]
+    code = _dtype_code(logits, "logits")
+    return moon_route_config(R, S, E, K, code, flags, scale, loss_coef), R, S, E, K
 
 
 def _flags8(valid, n, dev):
@@ -423,10 +432,7 @@ def moon_route(logits, topk, weights, flags=0, scale=1.0, bias=None, valid=None,
     [R, S, K] int32 and weights [R, S, K] float32; the optional outputs are
     described at moon_route in include/moon.h.  workspace: a uint8 tensor of at
     least moon_route_workspace(...) bytes; allocated for the call when None."""
-    if topk.dim() != 3 or topk.shape[:2] != logits.shape[:2]:
-        raise ValueError(f"topk must be [R, S, K], got {tuple(topk.shape)}")
-    cfg = _route_config(logits, topk.shape[2], flags, scale, loss_coef)
-    R, S, E, K = cfg.R, cfg.S, cfg.E, cfg.K
+    cfg, R, S, E, K = _route_config(logits, topk, flags, scale, loss_coef)
     dev, i32, f32 = _device_of(logits, "logits"), torch.int32, torch.float32
     if workspace is None and S > 32 and not (tokens_per_expert is None and valid_tokens is None
                                               and prob_sums is None and loss is None):
@@ -457,10 +463,7 @@ def moon_route_backward(logits, topk, d_logits, flags=0, scale=1.0, valid=None, 
                         stream=None):
     """Gradient of moon_route to d_logits (the shape and dtype of logits) from
     d_weights [R, S, K] and d_loss [R], either of which may be None."""
-    if topk.dim() != 3 or topk.shape[:2] != logits.shape[:2]:
-        raise ValueError(f"topk must be [R, S, K], got {tuple(topk.shape)}")
-    cfg = _route_config(logits, topk.shape[2], flags, scale, loss_coef)
-    R, S, E, K = cfg.R, cfg.S, cfg.E, cfg.K
+    cfg, R, S, E, K = _route_config(logits, topk, flags, scale, loss_coef)
     dev, i32, f32 = _device_of(logits, "logits"), torch.int32, torch.float32
     _call(dev, _lib.moon_route_backward, ctypes.byref(cfg),
           _addr(logits, logits.dtype, R * S * E, "logits", dev), _flags8(valid, R * S, dev),
