@@ -436,8 +436,10 @@ def moon_route(logits, topk, weights, flags=0, scale=1.0, bias=None, valid=None,
     dev, i32, f32 = _device_of(logits, "logits"), torch.int32, torch.float32
     if workspace is None and S > 32 and not (tokens_per_expert is None and valid_tokens is None
                                               and prob_sums is None and loss is None):
-        n = moon_route_workspace(R, S, E, K)
-        if n > 0:  # from the pool of the stream that uses it, so nothing else still does
+        n = _route_workspace(cfg)
+        if n > 0 and stream is None:
+            workspace = torch.empty(n, dtype=torch.uint8, device=logits.device)
+        elif n > 0:  # from the pool of the stream that uses it, so nothing else still does
             with torch.cuda.stream(stream):
                 workspace = torch.empty(n, dtype=torch.uint8, device=logits.device)
     ws_bytes = 0 if workspace is None else workspace.numel()
@@ -450,12 +452,15 @@ def moon_route(logits, topk, weights, flags=0, scale=1.0, bias=None, valid=None,
           _opt(workspace, torch.uint8, ws_bytes, "workspace", dev), ws_bytes, stream=stream)
 
 
-def moon_route_workspace(R, S, E, K):
-    """Bytes of workspace that moon_route needs for these sizes."""
-    cfg = moon_route_config(R, S, E, K, MOON_DTYPE_F32, 0, 1.0, 0.0)
+def _route_workspace(cfg):
     n = _sz(0)
     _check(_lib.moon_route_workspace(ctypes.byref(cfg), ctypes.byref(n)), "moon_route_workspace")
     return n.value
+
+
+def moon_route_workspace(R, S, E, K):
+    """Bytes of workspace that moon_route needs for these sizes."""
+    return _route_workspace(moon_route_config(R, S, E, K, MOON_DTYPE_F32, 0, 1.0, 0.0))
 
 
 def moon_route_backward(logits, topk, d_logits, flags=0, scale=1.0, valid=None, d_weights=None,
