@@ -399,3 +399,34 @@ def test_route_most_tokens(env):
     torch.cuda.synchronize()
     for a in range(0, S, 2 ** 28):  # a softmax over one expert has no gradient
         assert float(d[0, a:a + 2 ** 28].float().abs().max()) == 0.0
+
+
+@pytest.mark.parametrize("S", [7, 300])
+def test_route_infinite_biases(env, S):
+    """A bias of infinity forces an expert, -infinity leaves it to the last, NaN
+    behind those; the scores stay what they were."""
+    moon, torch, dev = env
+    say(f"[case] infinite biases S={S}")
+    rng = np.random.default_rng(S)
+    E, K = 96, 8
+    x = rng.standard_normal((1, S, E)).astype(np.float32)
+    x[0, 1, :60] = -np.inf
+    for forced, out, nan in [([5, 70, 3], range(20, 40), [0]), (range(0, 90, 7), [1], []),
+                             ([], range(0, 90), [91, 92]), ([2], range(3, 96), [])]:
+        bias = np.round(rng.standard_normal(E) * 8).astype(np.float32) / 8
+        bias[list(forced)], bias[list(out)], bias[list(nan)] = np.inf, -np.inf, np.nan
+        topk = torch.empty((1, S, K), dtype=torch.int32, device=dev)
+        w = torch.empty((1, S, K), device=dev)
+        moon.moon_route(torch.from_numpy(x).to(dev), topk, w, moon.MOON_ROUTE_SIGMOID | moon.MOON_ROUTE_RENORM,
+                        bias=torch.from_numpy(bias).to(dev))
+        torch.cuda.synchronize()
+        z = x[0].astype(np.float64)
+        s = 1.0 / (1.0 + np.exp(-z))
+        key = np.where(np.isneginf(z), -np.inf, s + bias)
+        order = np.lexsort((np.broadcast_to(np.arange(E), key.shape),
+                            -np.where(np.isnan(key), 0.0, key), np.isnan(key)))[:, :K]
+        assert (topk.cpu().numpy()[0] == order).all()
+        sel = np.take_along_axis(s, order, 1)
+        want = sel / np.where(sel.sum(1) > 0, sel.sum(1), 1.0)[:, None]
+        # a score's exponent and reciprocal, the sum's K terms, the division
+        assert (np.abs(w.double().cpu().numpy()[0] - want) <= (K + 2 * 6 + 64) * EPS * want + 1e-37).all()
