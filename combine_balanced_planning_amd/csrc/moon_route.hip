@@ -672,11 +672,13 @@ __global__ void __launch_bounds__(256) k_route_grad(RouteGradArgs a, int nblk) {
 
 // How a call is cut: waves per workgroup and workgroups per rank.  Up to 32
 // tokens a rank one workgroup of 16 waves does it all in one launch, at most
-// two tokens a wave; beyond that workgroups of eight waves, four to a compute
-// unit (1024 in all), and a second launch of 5 to 7 us adds their partial sums
-// (R=8, E=256 with a bias: 32 tokens 9.2 us in one launch and 10.3 in two, 48
-// tokens 11.0 and 10.4, 64 tokens 13.6 and 10.3).  Without counts, sums or loss
-// there is nothing to add and every four tokens get a workgroup.
+// two tokens a wave; beyond that workgroups of 16 waves, two to a compute unit
+// (512 in all; 1024 of eight waves leave twice the partial sums: 67 against
+// 65.5 us at R=16, S=8192, E=384, 25.1 against 24.3 at R=8, S=4096, E=256), and
+// a second launch of 4 to 5 us adds their partial sums (R=8, E=256 with a bias:
+// 32 tokens 9.2 us in one launch and 10.3 in two, 48 tokens 11.0 and 10.4, 64
+// tokens 13.6 and 10.3).  Without counts, sums or loss there is nothing to add
+// and every four tokens get a workgroup.
 constexpr int kOneLaunchTokens = 32;
 
 void route_cut(int R, int S, bool stats, int* waves, int* nblk) {
@@ -685,9 +687,9 @@ void route_cut(int R, int S, bool stats, int* waves, int* nblk) {
     *nblk = 1;
     return;
   }
-  *waves = stats ? 8 : 4;
+  *waves = stats ? kMaxWaves : 4;
   const int want = (int)(((int64_t)S + *waves - 1) / *waves);
-  *nblk = std::min(want, stats ? std::max(2, 1024 / R) : 65536);
+  *nblk = std::min(want, stats ? std::max(2, 512 / R) : 65536);
 }
 
 size_t route_workspace(int R, int S, int E, bool stats) {
