@@ -539,6 +539,11 @@ __global__ void __launch_bounds__(1024) k_route_finish(RouteArgs a, int experts)
   });
 }
 
+// HBM bounds it: the logits once and their gradient once.  8192 workgroups: at
+// R=16, S=8192, E=384, fp32 (0.4 GB) 79 us by itself and 138 with the forward
+// before it; 4096 finish less evenly (82 and 142), 16384 are set up too often
+// (84).  Stores past the caches help it alone (75) and not behind the forward
+// (140), and a reader of the gradient would miss them.
 template <int J, bool BF16>
 __global__ void __launch_bounds__(256) k_route_grad(RouteGradArgs a, int nblk) {
   __shared__ float lds[4][J * kLanes];  // a wave's experts, by id
@@ -739,7 +744,7 @@ hipError_t run_route(const RouteArgs& a, int waves, hipStream_t s) {
 
 template <int J, bool BF16>
 hipError_t run_route_grad(const RouteGradArgs& a, hipStream_t s) {
-  const int nblk = std::max(1, std::min((int)(((int64_t)a.S + 3) / 4), 4096 / a.R));
+  const int nblk = std::max(1, std::min((int)(((int64_t)a.S + 3) / 4), 8192 / a.R));
   hipLaunchKernelGGL((k_route_grad<J, BF16>), dim3(nblk, a.R), dim3(256), 0, s, a, nblk);
   return hipGetLastError();
 }
