@@ -603,6 +603,7 @@ __global__ void __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_
     fill(st3, 0, 3);
     if (!Whole) put_scales(0, v);
   }
+  wait_vm<0>();  // this wave's part is in LDS before the others read it
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 6; ++i)
