@@ -628,16 +628,15 @@ __global__ void __launch_bounds__(256) k_route_grad(RouteGradArgs a, int nblk) {
         wave_lds_sync();
 #pragma unroll
         for (int j = 0; j < J; ++j) at_id[j * kLanes + lane] = 0.0f;
+        // s * dL/ds from the quotient: sums of small sigmoids have reciprocals
+        // near the end of fp32, and a gradient times one would pass it
         float g;
         if (a.renorm) {
-          const float rn = reciprocal_or_zero(wave_sum(sel));
-          const float mean = wave_sum(dw * (sel * rn));
-          g = a.scale * rn * (dw - mean);
+          const float share = sel * reciprocal_or_zero(wave_sum(sel));
+          g = a.scale * share * (dw - wave_sum(dw * share));
         } else {
-          g = a.scale * dw;
+          g = a.scale * dw * (a.sigmoid ? sel : sel * inv);
         }
-        // softmax scores are inv times the ones above
-        if (!a.sigmoid && !a.renorm) g *= inv;
         wave_lds_sync();
         if (picked) atomicAdd(&at_id[id], g);
         wave_lds_sync();
@@ -648,18 +647,18 @@ __global__ void __launch_bounds__(256) k_route_grad(RouteGradArgs a, int nblk) {
 #pragma unroll
         for (int j = 0; j < J; ++j) d[j] = 0.0f;
       }
-      // d is dL/ds of the scores s here, p = s * inv
+      // d is s times the weights' part of dL/ds here; p = s * inv
       float dot = 0.0f;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         dot = fmaf(s[j] * inv, b[j], dot);
-        if (!a.sigmoid) dot = fmaf(s[j], d[j], dot);
+        if (!a.sigmoid) dot += d[j];
       }
       dot = wave_sum(dot);
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        const float ds = d[j] + (b[j] - dot) * inv;
-        d[j] = (a.sigmoid ? s[j] * logistic(-x[j]) : s[j]) * ds;
+        const float sds = fmaf(s[j] * inv, b[j] - dot, d[j]);
+        d[j] = a.sigmoid ? sds * logistic(-x[j]) : sds;
       }
     }
 #pragma unroll
