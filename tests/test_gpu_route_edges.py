@@ -81,6 +81,50 @@ def check(env, x, K, sigmoid, renorm, scale=1.0, bias=None, valid=None, dw_scale
     return topk, w, P, loss, d
 
 
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("S", [9, 40])
+def test_masks_by_token(env, sigmoid, renorm, S):
+    """Masks of -infinity and of the type's lowest value beside each other: rows
+    with fewer than K experts left, one, none."""
+    print(f"[case] masks by token sigmoid={sigmoid} renorm={renorm} S={S}", flush=True)
+    rng = np.random.default_rng(16)
+    low, high = np.finfo(np.float32).min, np.finfo(np.float32).max
+    x = rng.standard_normal((2, S, 70)).astype(np.float32)
+    x[rng.random(x.shape) < 0.4] = -np.inf
+    x[rng.random(x.shape) < 0.2] = low
+    x[0, 3], x[0, 4, 1:], x[1, 7, :66], x[1, 8] = -np.inf, -np.inf, -np.inf, low
+    x[1, 5, 3:], x[0, 6, 2], x[1, 2, :] = low, high, 60.0
+    check(env, x, 8, sigmoid, renorm)
+    if sigmoid:
+        check(env, x, 8, sigmoid, renorm, bias=rng.standard_normal(70).astype(np.float32))
+
+
+@pytest.mark.parametrize("S", [31, 32, 33, 34])
+@pytest.mark.parametrize("E,K,sigmoid", [(24, 3, False), (256, 8, True), (320, 40, True)])
+def test_around_the_second_launch(env, S, E, K, sigmoid):
+    """All outputs at the most tokens of one launch and the fewest of two."""
+    print(f"[case] S={S} E={E} K={K} sigmoid={sigmoid}", flush=True)
+    rng = np.random.default_rng(S)
+    x = (2 * rng.standard_normal((3, S, E))).astype(np.float32)
+    bias = (0.1 * rng.standard_normal(E)).astype(np.float32) if sigmoid else None
+    valid = rng.random((3, S)) < 0.8
+    valid[2] = False
+    valid[1, :-1] = False
+    for v in (None, valid):
+        check(env, x, K, sigmoid, True, 2.5, bias=bias, valid=v)
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+def test_wide_logits(env, renorm):
+    """Logits from -100 to 100: scores of 1 and scores far below."""
+    rng = np.random.default_rng(3)
+    x = rng.uniform(-100, 100, (2, 50, 96)).astype(np.float32)
+    for sigmoid in (False, True):
+        print(f"[case] wide logits sigmoid={sigmoid} renorm={renorm}", flush=True)
+        check(env, x, 6, sigmoid, renorm)
+
+
 @pytest.mark.parametrize("K,E", [(2, 8), (1, 5), (8, 128)])
 @pytest.mark.parametrize("at", [-60.0, -80.0, -86.0])
 def test_gradient_of_small_sigmoids(env, K, E, at):
@@ -91,3 +135,18 @@ def test_gradient_of_small_sigmoids(env, K, E, at):
     rng = np.random.default_rng(E)
     x = (at + 0.3 * rng.standard_normal((2, 40, E))).astype(np.float32)
     check(env, x, K, True, True, 2.5, dw_scale=65536.0, coef=1.0)
+
+
+def test_sigmoids_that_count_as_zero(env):
+    """Sigmoids below 2^-126 throughout: ids by the logits, all else 0."""
+    moon, torch, dev = env
+    x = torch.linspace(-120, -90, 40, device=dev).repeat(1, 5, 1).contiguous()
+    topk = torch.empty((1, 5, 4), dtype=torch.int32, device=dev)
+    w, P, loss = torch.ones((1, 5, 4), device=dev), torch.ones((1, 40), device=dev), torch.ones(1, device=dev)
+    c, n, d = torch.empty((1, 40), dtype=torch.int32, device=dev), torch.empty(1, dtype=torch.int32, device=dev), \
+        torch.ones_like(x)
+    moon.moon_route(x, topk, w, 3, 2.5, tokens_per_expert=c, valid_tokens=n, prob_sums=P, loss=loss, loss_coef=1.0)
+    moon.moon_route_backward(x, topk, d, 3, 2.5, d_weights=torch.ones_like(w), tokens_per_expert=c, valid_tokens=n,
+                             d_loss=torch.ones(1, device=dev), loss_coef=1.0)
+    assert topk[0].tolist() == [[39, 38, 37, 36]] * 5
+    assert all(float(a.abs().max()) == 0.0 for a in (w, P, loss, d))
