@@ -292,13 +292,13 @@ typedef enum { MOON_DTYPE_F32 = 0, MOON_DTYPE_BF16 = 1 } moon_dtype;
 
 /* Routing flags.  Scores are softmax(logits), or 1/(1+exp(-logit)) with
  * MOON_ROUTE_SIGMOID; MOON_ROUTE_RENORM divides a token's K weights by their
- * sum. */
+ * sum.  A sigmoid below 2^-126 (a logit below -87.3) counts as 0. */
 #define MOON_ROUTE_SIGMOID 0x1u
 #define MOON_ROUTE_RENORM 0x2u
 
 /* R ranks of S tokens with E logits each, K experts per token; dtype (a
- * moon_dtype) is that of the logits and their gradient.  Limits: R <= 32,
- * K <= E <= 512, K <= 64, R*S*K < 2^31. */
+ * moon_dtype) is that of the logits and their gradient.  Limits: every size at
+ * least 1, R <= 32, K <= E <= 512, K <= 64, R*S*K < 2^31. */
 typedef struct {
   int32_t R, S, E, K, dtype;
   uint32_t flags;
@@ -310,15 +310,16 @@ typedef struct {
  * for any set of outputs. */
 moon_status moon_route_workspace(const moon_route_config* cfg, size_t* bytes);
 
-/* Top-k routing.  For every token: topk_rsk [R,S,K] the ids of its K largest
- * logits, in descending order, the lower id first among equals (with bias_e
- * [E] fp32, MOON_ROUTE_SIGMOID only: of its K largest score + bias), and
- * weights_rsk [R,S,K] fp32 = scale * score (divided by their sum with
- * MOON_ROUTE_RENORM).  Two ids of a token never agree.  A logit of -infinity
+/* Top-k routing over all E experts (no groups of them are chosen first).  For
+ * every token: topk_rsk [R,S,K] the ids of its K largest logits, in descending
+ * order, the lower id first among equals (with bias_e [E] fp32,
+ * MOON_ROUTE_SIGMOID only: of its K largest score + bias), and weights_rsk
+ * [R,S,K] fp32 = scale * score (divided by their sum with MOON_ROUTE_RENORM).  Two ids of a token never agree.  A logit of -infinity
  * masks its expert: score 0, picked only when fewer than K others are left; a
- * sum of scores that is 0 gives weights 0.  A NaN logit ranks last
- * and makes NaN what its score enters (weights renormalised over picked
- * experts only where it is picked).
+ * sum of scores that is 0 gives weights 0, and no part in prob_sums_re.  A NaN
+ * logit ranks last and makes NaN what its score enters (weights renormalised
+ * over picked experts only where it is picked); a logit of +infinity makes a
+ * softmax NaN.
  * valid_rs [R,S] (optional): a 0 marks a token outside the batch, whose logits
  * have no effect (NaN neither), whose ids and weights are 0 and which the balance
  * leaves out.
@@ -341,7 +342,9 @@ moon_status moon_route(const moon_route_config* cfg, const void* logits_rse, con
 /* Gradient of moon_route: d_logits_rse [R,S,E] (written whole) from
  * d_weights_rsk [R,S,K] fp32 (or NULL) at the ids topk_rsk, and from d_loss_r
  * [R] fp32 (or NULL) with the counts and valid tokens that moon_route wrote.
- * The ids and counts carry no gradient; tokens outside the batch get 0. */
+ * The ids and counts carry no gradient; tokens outside the batch get 0.  A
+ * token's ids differ, as moon_route writes them (one outside [0,E) is left
+ * out); then results repeat bit for bit. */
 moon_status moon_route_backward(const moon_route_config* cfg, const void* logits_rse,
                                 const uint8_t* valid_rs, const int32_t* topk_rsk,
                                 const float* d_weights_rsk, const int32_t* tokens_per_expert_re,
@@ -361,8 +364,10 @@ moon_status moon_mx4_quantize(const void* x, int32_t dtype, int64_t rows, int32_
                               const moon_plan_arrays* plan, uint8_t* q, uint8_t* scales,
                               hipStream_t stream);
 
-/* The values that q and scales stand for, to y [rows, cols] of dtype (exact;
- * NaN where the scale byte is 255). */
+/* The values that q and scales stand for, to y [rows, cols] of dtype: exact;
+ * NaN where the scale byte is 255, infinity for a magnitude of 2^128 or more
+ * (only under the scale bytes 253 and 254, which moon_mx4_quantize never
+ * writes). */
 moon_status moon_mx4_dequantize(const uint8_t* q, const uint8_t* scales, int64_t rows,
                                 int32_t cols, const moon_plan_arrays* plan, int32_t dtype,
                                 void* y, hipStream_t stream);
@@ -371,7 +376,9 @@ moon_status moon_mx4_dequantize(const uint8_t* q, const uint8_t* scales, int64_t
  * copies codes and scales into the slots as two of its tensors):
  *   expert_q [E, N, K/2], expert_scales [E, N, K/32]        the experts
  *   slot_q [R, B, N, K/2], slot_scales [R, B, N, K/32]      the slots
- * codes 16-byte aligned. */
+ * codes 16-byte aligned.  moon_prefetch_weight copies rows of a multiple of 16
+ * bytes: where N*K is no multiple of 512 the scales' rows have to be padded for
+ * it, and laid out as above afterwards. */
 typedef struct {
   const uint8_t *expert_q, *expert_scales, *slot_q, *slot_scales;
 } moon_mx4_weight;
@@ -379,7 +386,9 @@ typedef struct {
 /* Product of every group's rows with its expert's weight: y [R*NvS, N] bf16,
  * y[row][n] = sum over k of x[row][k] * w[n][k], summed in fp32 and rounded
  * once; x = (xq, xs) as moon_mx4_quantize writes window rows.  K is a
- * multiple of 32, N of 8, both at most 65536. */
+ * multiple of 32, N of 8, both at most 65536.  Fastest with K a multiple of 512
+ * (others take as long as the next multiple does, or up to 27 % longer)
+ * and, for many rows, with R*(E/R + B) at most 1024 (a third longer beyond). */
 moon_status moon_expert_gemm_mx4(const moon_plan_arrays* plan, const uint8_t* xq,
                                  const uint8_t* xs, int32_t K, const moon_mx4_weight* w, int32_t N,
                                  void* y, hipStream_t stream);
@@ -398,7 +407,8 @@ moon_status moon_expert_swiglu_mx4(const moon_plan_arrays* plan, const uint8_t* 
  * exp(-g)) * u, c = row_weights[row] or 1, and saved [R*NvS, 2F] with
  * saved_scales [R*NvS, 2F/32]: e4m3 values, 32 of them under the smallest
  * scale 2^(byte - 127) that holds the largest (at most 448 of it), rounded to
- * nearest even; byte 255 marks a block with an infinity or a NaN.  saved is
+ * nearest even; byte 255 marks a block with an infinity or a NaN, and a
+ * magnitude from 1.9375 * 2^127 on, nearest to 2^128, reads back as infinity.  saved is
  * not written at padding rows.  F is a multiple of 32, at most 65536; gate_up,
  * h and saved 16-byte aligned. */
 moon_status moon_swiglu_save8(const moon_plan_arrays* plan, const void* gate_up,
