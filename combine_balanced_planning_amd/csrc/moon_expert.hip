@@ -368,16 +368,19 @@ __device__ __forceinline__ void half_step(const vec4u* wsrc, const vec4u* xsrc, 
 // of the next turn, which may belong to the next tile: the loads run three
 // steps ahead without a pause at tile borders.
 //
-// Gate and up products of 262144 rows, K=7168, F=2048 in 288 groups take 4.25 ms
-// (3.6 PFLOP/s, 4.1 with the unused rows of the groups' last tiles) at a clock
-// that the power limit holds near 1.65 GHz; a library's product of two 16384 x
-// 16384 MXFP4 matrices reaches 3.2 PFLOP/s on the same card.  Tried and slower:
+// Gate and up products of 262144 rows, K=7168, F=2048 in 288 groups take 4.2 ms
+// (3.7 PFLOP/s, 4.2 with the unused rows of the groups' last tiles, 12 % of the
+// tiles' rows); a library's product of two 16384 x 16384 MXFP4 matrices reaches
+// 3.2 PFLOP/s on the same card.  The matrix cores are busy 60 % of the cycles, and
+// the clock, 2.4 GHz at most, is 1.5 to 1.7 GHz under this load (2.1 under slower
+// variants of it).  Tried and slower:
 // four waves of 128 by 128 (256 accumulators: spills, or waits that drain the
 // loads), 128 bytes of a row a load with two steps ahead, loads into the caches
 // further ahead, a raised wave priority, leaving out the products of rows that
 // a last tile lacks.
-// Products of K=1024 (98304 rows, N=2048, 72 groups) take 195 us: 123 without
-// the epilogue, 148 with its stores dropped.  No faster there: the next tile's
+// Products of K=1024 (98304 rows, N=2048, 97 groups) take 186 to 197 us; in one
+// run 195, of which 123 without the epilogue and 148 with its stores dropped.  No
+// faster there: the next tile's
 // first steps not waiting for the stores, whole cache lines a store (205 us),
 // non-temporal stores (202 us).
 template <bool Swiglu, bool Whole>
@@ -746,6 +749,9 @@ moon_status launch(const ExpertArgs& a, const Groups& g, hipStream_t s) {
   //   2 rows 320/367/415, 8 rows 420/472/537, 16 rows 477/474/550,
   //   32 rows 663/513/578, 64 rows 1107/647/591, 128 rows 2087/1041/667.
   // The counts themselves are on the GPU; any group is right in any kernel.
+  // More entries than the tile table holds go by 64 rows at a time (R=32, E=512,
+  // 128 rows an expert, K=2048, gate and up to N=1024: 513 us by tiles with 1024
+  // entries, 690 with 1056).
   const int64_t rows = (int64_t)g.R * g.N;
   if (rows >= 48 * (int64_t)g.E && g.R * g.per <= kMaxEntries) {
     int dev = 0, cus = 256;
@@ -762,6 +768,13 @@ moon_status launch(const ExpertArgs& a, const Groups& g, hipStream_t s) {
       hipLaunchKernelGGL((k_expert_tiles<Swiglu, false>), dim3(wgs), dim3(kTileThreads), 0, s, a, g);
     return hipGetLastError() == hipSuccess ? MOON_OK : MOON_ERR_HIP;
   }
+  // K that is not whole turns of 512 values has its row's last scales read byte
+  // by byte, in either kind of kernel, and costs as much as the next whole K or
+  // more (us; whole K last):
+  //   16 rows at a time, R=8, E=256, S=16, N=7168: K=1056 350, 1408 408, 1536 325;
+  //     2880 702, 3584 696
+  //   tiles, R=8, E=256, S=4096, gate and up to N=2048: K=1056 1357, 1408 1380,
+  //     1536 1250; 2880 2456, 3584 2297
   const dim3 grid(Swiglu ? (a.N + 31) / 32 : (a.N + 63) / 64, g.R * g.per);
   const bool few = rows <= 12 * (int64_t)g.E;
   if (a.K % 512 == 0) {

@@ -18,9 +18,8 @@
 // largest of the lanes' maxima bounds the K-th largest value from below; bisection
 // of its bits with a ballot a round finds it.  The values that reach it, K and a
 // few more, are packed into lanes and ranked by comparing all pairs.  All but
-// the maxima and the picks are compared as the numbers they are: an integer key
-// for every expert took a third more vector instructions (44 against 39 us a
-// call at R=8, S=4096, E=256 with a bias).
+// the maxima and the picks are compared as the numbers they are (an integer key
+// for every expert takes a third more vector instructions).
 // Sums over tokens are kept per wave in registers, then per workgroup in LDS,
 // then per workgroup in the workspace, and added in a fixed order at each step,
 // so results repeat bit for bit.
@@ -210,8 +209,9 @@ __device__ __forceinline__ void finish_rank(const RouteArgs& a, int r, int n, fl
 }
 
 // The kernel's arguments, read again: what only the end of k_route needs would
-// else sit in scalar registers through its loop and push others out (36
-// spilled against 15, 77 against 73 us a call at the size below).
+// else sit in scalar registers through its loop and push others out (147
+// against 145 us a training step at R=16, S=8192, E=384, softmax; the biased
+// kernel, which spills vector registers, takes 227 and would take 222 without).
 __device__ __forceinline__ RouteArgs late_args() {
   const __attribute__((address_space(4))) RouteArgs* p =
       (const __attribute__((address_space(4))) RouteArgs*)__builtin_amdgcn_kernarg_segment_ptr();
@@ -233,12 +233,17 @@ __device__ __forceinline__ RouteArgs late_args() {
 }
 
 // Held to 64 registers for eight waves a SIMD: a token is a chain of dependent
-// steps, and more waves hide it (an earlier version took 113 us with fewer and
-// 96 with eight).  What selects, whether sums over tokens (or a token's sum of
-// scores) are wanted and whether the words are full are template arguments:
-// told at run time they cost branches and spilled scalars, 96 against 77 us a
-// call at R=16, S=8192, E=384, fp32 (67 now).  There the kernel takes 63 us, the
-// vector unit busy 72 % of them; the logits alone take 41 us to read.
+// steps, and more waves hide it.  What selects, whether sums over tokens (or a
+// token's sum of scores) are wanted and whether the words are full are template
+// arguments: told at run time they cost branches and spilled scalars.
+// At R=16, S=8192, E=384, fp32, softmax with sums the kernel takes 64 to 72
+// us, the vector unit busy 72 % of the shorter with 221 vector and 159 scalar instructions a
+// token; the logits alone take 41 us to read.  With four waves a SIMD a training
+// step there takes 158 us against 145, a prefill at R=8, S=4096, E=256 with a
+// bias 28.4 against 24.8.  The biased kernels with sums are the exception: they
+// need more than 64 registers (15 spilled at E=256, 25 at E=384, 42 at E=512)
+// and a training step takes 227 us at E=384 and 54 at E=256, with four waves
+// 159 and 49.
 template <int J, bool BF16, int Score, bool Sums, bool Whole>
 __global__ void __launch_bounds__(kMaxWaves* kLanes) __attribute__((amdgpu_waves_per_eu(8)))
     k_route(RouteArgs a) {
@@ -539,11 +544,10 @@ __global__ void __launch_bounds__(1024) k_route_finish(RouteArgs a, int experts)
   });
 }
 
-// HBM bounds it: the logits once and their gradient once.  8192 workgroups: at
-// R=16, S=8192, E=384, fp32 (0.4 GB) 79 us by itself and 138 with the forward
-// before it; 4096 finish less evenly (82 and 142), 16384 are set up too often
-// (84).  Stores past the caches help it alone (75) and not behind the forward
-// (140), and a reader of the gradient would miss them.
+// HBM bounds it: the logits once and their gradient once, 0.4 GB at R=16,
+// S=8192, E=384, fp32 in 75 us (5.4 TB/s).  8192 workgroups at most: with the
+// forward before it a step takes 145 us, with 4096 the same within 1 us, with
+// 16384, set up too often, 153.
 template <int J, bool BF16>
 __global__ void __launch_bounds__(256) k_route_grad(RouteGradArgs a, int nblk) {
   __shared__ float lds[4][J * kLanes];  // a wave's experts, by id
@@ -638,7 +642,7 @@ __global__ void __launch_bounds__(256) k_route_grad(RouteGradArgs a, int nblk) {
           g = a.scale * dw * (a.sigmoid ? sel : sel * inv);
         }
         wave_lds_sync();
-        if (picked) atomicAdd(&at_id[id], g);
+        if (picked) atomicAdd(&at_id[id], g);  // a token's ids differ: no order
         wave_lds_sync();
 #pragma unroll
         for (int j = 0; j < J; ++j) d[j] = at_id[j * kLanes + lane];
@@ -677,12 +681,12 @@ __global__ void __launch_bounds__(256) k_route_grad(RouteGradArgs a, int nblk) {
 // How a call is cut: waves per workgroup and workgroups per rank.  Up to 32
 // tokens a rank one workgroup of 16 waves does it all in one launch, at most
 // two tokens a wave; beyond that workgroups of 16 waves, two to a compute unit
-// (512 in all; 1024 of eight waves leave twice the partial sums: 67 against
-// 65.5 us at R=16, S=8192, E=384, 25.1 against 24.3 at R=8, S=4096, E=256), and
-// a second launch of 4 to 5 us adds their partial sums (R=8, E=256 with a bias:
-// 32 tokens 9.2 us in one launch and 10.3 in two, 48 tokens 11.0 and 10.4, 64
-// tokens 13.6 and 10.3).  Without counts, sums or loss there is nothing to add
-// and every four tokens get a workgroup.
+// (512 in all; 1024 of eight waves take the same within 1 us at R=16, S=8192,
+// E=384 and leave twice the partial sums), and a second launch of 4 to 5 us adds
+// their partial sums (calls of the binding, R=8, E=256, bf16 with a bias: 32
+// tokens 8.4 us in one launch, 48 tokens 10.2 in one and 12 to 13 in two, 64
+// tokens 12.8 and 12 to 13).  Without counts, sums or loss there is nothing to
+// add and every four tokens get a workgroup.
 constexpr int kOneLaunchTokens = 32;
 
 void route_cut(int R, int S, bool stats, int* waves, int* nblk) {
